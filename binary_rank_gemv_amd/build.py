@@ -27,6 +27,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "liblittlebit.so")
 INIT_LIB = os.path.join(LIBDIR, "liblittlebit_init.so")
+HEAD_LIB = os.path.join(LIBDIR, "liblittlebit_head.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops keeps the compiler from emitting packed fp32 VALU forms.
@@ -38,10 +39,11 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 
 LAYER_SOURCES = ("decode.hip", "decode1.hip", "littlebit_host.hip", "pack.hip", "prefill.hip")
 INIT_SOURCES = ("init.hip",)
+HEAD_SOURCES = ("head_host.hip", "logprobs.hip", "norm.hip", "q8.hip")
 
 
 def sources():
-    return [os.path.join(CSRC, f) for f in LAYER_SOURCES + INIT_SOURCES]
+    return [os.path.join(CSRC, f) for f in LAYER_SOURCES + INIT_SOURCES + HEAD_SOURCES]
 
 
 def _run(cmd, verbose):
@@ -136,7 +138,7 @@ def build_phase_stamped(verbose: bool = False) -> str:
 
 
 def build_library(verbose: bool = False, extra_flags=()) -> str:
-    """Compile both libraries; returns the layer library's path."""
+    """Compile all libraries; returns the layer library's path."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = sources()
     with ThreadPoolExecutor(max_workers=min(len(srcs), 8)) as ex:
@@ -144,6 +146,7 @@ def build_library(verbose: bool = False, extra_flags=()) -> str:
                         ex.map(lambda s: _compile(s, verbose, extra_flags), srcs)))
     _link([objs[f] for f in LAYER_SOURCES], LIB, [], verbose)
     _link([objs[f] for f in INIT_SOURCES], INIT_LIB, ["-lrocblas", "-lrocsolver"], verbose)
+    _link([objs[f] for f in HEAD_SOURCES], HEAD_LIB, [], verbose)
     return LIB
 
 

@@ -1,0 +1,351 @@
+// Residual root-mean-square norm, its backward pass, and the row quantiser.
+//
+// Forward, per row:  h = round(x + res);  s2 = sum h^2;  a = max |h w|
+//     r = 1/sqrt(s2/n + eps);  y = (h w) r;  scale = a r / 127;
+//     q = rint(y / scale) = rint((h w) * 127 / a)
+// The largest |y| is a r, so both reductions run over the same values in one
+// exchange: the row is read once, held in registers, and the 8-bit codes need
+// no second reduction.  A group of G threads owns a row, thread t of it the
+// vectors t, t + G, ... of eight elements.
+#include "head_common.h"
+#include "head_launch.h"
+
+using namespace lbh;
+
+namespace {
+
+constexpr float kBig = 0x1p100f;
+
+// 127 / a without leaving the range for a tiny a: values are multiplied by
+// `up` first (exact, a power of two).
+struct Q8Scale {
+  float up, inv;
+};
+__device__ __forceinline__ Q8Scale q8_scale(float a) {
+  Q8Scale s;
+  s.up = a < 1e-30f ? kBig : 1.0f;
+  const float au = a * s.up;
+  // a row of zeros has codes 0
+  s.inv = (au > 0.0f && au < INFINITY) ? 127.0f / au : 0.0f;
+  return s;
+}
+__device__ __forceinline__ int q8_code(float v, const Q8Scale& s) {
+  const float c = rintf(v * s.up * s.inv);
+  return (int)fminf(fmaxf(c, -127.0f), 127.0f);
+}
+
+// `fine`: the row is finite (otherwise its codes are 0).
+__device__ __forceinline__ void q8_store(int8_t* p, long left, const float (&v)[8], const Q8Scale& s, bool fine) {
+  int c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = fine ? q8_code(v[i], s) : 0;
+  if (left >= 8) {
+    u32x2 w;
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+      w[d] = (uint32_t)(c[4 * d] & 255) | (uint32_t)(c[4 * d + 1] & 255) << 8 | (uint32_t)(c[4 * d + 2] & 255) << 16 |
+             (uint32_t)(c[4 * d + 3] & 255) << 24;
+    store_any(p, w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = (int8_t)c[i];
+  }
+}
+
+// Sum of `s` and maximum of `a` over a group of G threads (G = 64: a wave;
+// otherwise the whole workgroup).  A NaN in the row is in the sum.
+template <int G>
+__device__ __forceinline__ void group_reduce(float& s, float& a) {
+  s = wave_sum(s);
+  a = wave_max(a);
+  if constexpr (G > 64) {
+    __shared__ float part[2][G / 64];
+    const int w = wave_id(), lane = threadIdx.x & 63;
+    if (lane == 0) {
+      part[0][w] = s;
+      part[1][w] = a;
+    }
+    __syncthreads();
+    s = part[0][0];
+    a = part[1][0];
+#pragma unroll
+    for (int i = 1; i < G / 64; ++i) {
+      s += part[0][i];
+      a = fmaxf(a, part[1][i]);
+    }
+  }
+}
+
+// QUANT: the row quantiser alone (no residual, weight or norm).
+template <typename T, int G, int V, bool QUANT>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNormArgs A) {
+  constexpr int kPer = G < 256 ? 256 / G : 1;  // rows a workgroup
+  const int t = threadIdx.x % G;
+  const long row = (long)blockIdx.x * kPer + threadIdx.x / G;
+  if (row >= A.rows) return;  // whole waves only: G is a wave or the workgroup
+  const T* x = (const T*)A.x + row * A.ldx;
+  float h[V][8], hw[V][8];
+  float s2 = 0.0f, a = 0.0f;
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int k = 8 * (t + i * G);
+    const long left = A.n - k;
+    if (left > 0) {
+      load8(x + k, left, 0.0f, h[i]);
+      if constexpr (!QUANT) {
+        if (A.residual) {
+          float r[8];
+          load8((const T*)A.residual + row * A.ldr + k, left, 0.0f, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[i][e] = (float)(T)(h[i][e] + r[e]);
+        }
+        load8((const T*)A.weight + k, left, 0.0f, hw[i]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] = hw[i][e] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (QUANT) {
+        hw[i][e] = h[i][e];
+        s2 += h[i][e] * 0.0f;  // NaN where the row has a NaN or an infinity
+      } else {
+        hw[i][e] *= h[i][e];
+        s2 += h[i][e] * h[i][e];
+      }
+      a = fmaxf(a, fabsf(hw[i][e]));
+    }
+  }
+  if constexpr (!QUANT) {
+    if (A.hidden) {
+      T* hp = (T*)A.hidden + row * A.ldh;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int k = 8 * (t + i * G);
+        store8(hp + k, (long)A.n - k, h[i]);
+      }
+    }
+  }
+  group_reduce<G>(s2, a);
+  float r = 1.0f;
+  if constexpr (!QUANT) r = 1.0f / sqrtf(s2 / (float)A.n + A.eps);
+  const float top = QUANT ? a + s2 : a * r;  // s2 is 0 or NaN for the quantiser
+  fine = top < INFINITY;                     // false for NaN too
+  if (A.q) {
+    const Q8Scale sc = q8_scale(a);
+    int8_t* qp = A.q + row * A.ldq;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = 8 * (t + i * G);
+      q8_store(qp + k, (long)A.n - k, hw[i], sc, fine);
+    }
+    if (t == 0) A.scale[row] = fine ? top / 127.0f : NAN;
+  }
+  if constexpr (!QUANT) {
+    if (A.y) {
+      T* yp = (T*)A.y + row * A.ldy;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int k = 8 * (t + i * G);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = hw[i][e] * r;
+        store8(yp + k, (long)A.n - k, y);
+      }
+    }
+  }
+}
+
+template <typename T, int G, int V, bool QUANT>
+void launch_one(const LbNormArgs& a, hipStream_t stream) {
+  constexpr int per = G < 256 ? 256 / G : 1;
+  const long blocks = (a.rows + per - 1) / per;
+  hipLaunchKernelGGL((lb_norm_kernel<T, G, V, QUANT>), dim3((unsigned)blocks), dim3(G < 256 ? 256 : G), 0, stream, a);
+}
+
+template <typename T, bool QUANT>
+void launch_norm(const LbNormArgs& a, hipStream_t stream) {
+  if (a.n <= 512)
+    launch_one<T, 64, 1, QUANT>(a, stream);
+  else if (a.n <= 2048)
+    launch_one<T, 256, 1, QUANT>(a, stream);
+  else if (a.n <= 4096)
+    launch_one<T, 256, 2, QUANT>(a, stream);
+  else if (a.n <= 8192)
+    launch_one<T, 256, 4, QUANT>(a, stream);
+  else if (a.n <= 16384)
+    launch_one<T, 1024, 2, QUANT>(a, stream);
+  else
+    launch_one<T, 1024, 4, QUANT>(a, stream);
+}
+
+// -------------------------------------------------------------------- backward
+// With u = w dy:  dx = dhidden + r u - h (r^3 / n) sum(u h);  both sums
+// (h^2 for r, and u h) run over the row in one exchange, so r need not be kept
+// from the forward pass.  dweight = sum over rows of dy h r: a group keeps its
+// rows' sum in registers and writes it once; a second kernel adds the groups
+// in a fixed order.
+template <typename T, int G, int V>
+__global__ __launch_bounds__(G) void lb_norm_bwd_kernel(const LbNormBwdArgs A) {
+  __shared__ float part[2][2][G / 64];
+  const int t = threadIdx.x, w = wave_id(), lane = t & 63;
+  float wt[V][8], dw[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int k = 8 * (t + i * G);
+    if (k < A.n) {
+      load8((const T*)A.weight + k, (long)A.n - k, 0.0f, wt[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wt[i][e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  }
+  int flip = 0;
+  for (long row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
+    float h[V][8], dy[V][8], dh[V][8];
+    float s2 = 0.0f, uh = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = 8 * (t + i * G);
+      const long left = A.n - k;
+      if (left > 0) {
+        load8((const T*)A.hidden + row * A.ldh + k, left, 0.0f, h[i]);
+        load8((const T*)A.dy + row * A.lddy + k, left, 0.0f, dy[i]);
+        if (A.dhidden) load8((const T*)A.dhidden + row * A.lddh + k, left, 0.0f, dh[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = dy[i][e] = 0.0f;
+      }
+      if (!A.dhidden || left <= 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dh[i][e] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s2 += h[i][e] * h[i][e];
+        uh += wt[i][e] * dy[i][e] * h[i][e];
+      }
+    }
+    s2 = wave_sum(s2);
+    uh = wave_sum(uh);
+    if (lane == 0) {
+      part[flip][0][w] = s2;
+      part[flip][1][w] = uh;
+    }
+    __syncthreads();  // two buffers in turn: one barrier a row is enough
+    s2 = part[flip][0][0];
+    uh = part[flip][1][0];
+#pragma unroll
+    for (int i = 1; i < G / 64; ++i) {
+      s2 += part[flip][0][i];
+      uh += part[flip][1][i];
+    }
+    const float r = 1.0f / sqrtf(s2 / (float)A.n + A.eps);
+    const float c = (uh * r) * r / (float)A.n;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = 8 * (t + i * G);
+      float d[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float hr = h[i][e] * r;
+        d[e] = dh[i][e] + (r * (wt[i][e] * dy[i][e]) - hr * c);
+        dw[i][e] += dy[i][e] * hr;
+      }
+      store8((T*)A.dx + row * A.lddx + k, (long)A.n - k, d);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int k = 8 * (t + i * G);
+    store8(A.partial + (long)blockIdx.x * A.n + k, (long)A.n - k, dw[i]);
+  }
+}
+
+// dweight = sum of the groups' partial sums: 32 columns x 32 slices of groups
+// a workgroup, slices joined in order.
+__global__ __launch_bounds__(1024) void lb_norm_dweight_kernel(const float* __restrict__ partial, int groups, int n,
+                                                               float* __restrict__ dweight) {
+  __shared__ float s[32][33];
+  const int c = threadIdx.x & 31, p = threadIdx.x >> 5;
+  const int k = blockIdx.x * 32 + c;
+  float v = 0.0f;
+  if (k < n)
+    for (int g = p; g < groups; g += 32) v += partial[(long)g * n + k];
+  s[p][c] = v;
+  __syncthreads();
+  if (p == 0 && k < n) {
+    v = s[0][c];
+    for (int i = 1; i < 32; ++i) v += s[i][c];
+    dweight[k] = v;
+  }
+}
+
+template <typename T, int G, int V>
+void launch_bwd_one(const LbNormBwdArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((lb_norm_bwd_kernel<T, G, V>), dim3((unsigned)a.groups), dim3(G), 0, stream, a);
+}
+
+template <typename T>
+void launch_bwd(const LbNormBwdArgs& a, hipStream_t stream) {
+  if (a.n <= 2048)
+    launch_bwd_one<T, 256, 1>(a, stream);
+  else if (a.n <= 4096)
+    launch_bwd_one<T, 512, 1>(a, stream);
+  else if (a.n <= 8192)
+    launch_bwd_one<T, 1024, 1>(a, stream);
+  else if (a.n <= 16384)
+    launch_bwd_one<T, 1024, 2>(a, stream);
+  else
+    launch_bwd_one<T, 1024, 4>(a, stream);
+}
+
+}  // namespace
+
+hipError_t lb_launch_norm(const LbNormArgs& a, int dtype, hipStream_t stream) {
+  if (dtype == 1)
+    launch_norm<f16, false>(a, stream);
+  else
+    launch_norm<bf16, false>(a, stream);
+  return hipGetLastError();
+}
+
+hipError_t lb_launch_q8_quantize(const LbNormArgs& a, int dtype, hipStream_t stream) {
+  if (dtype == 0)
+    launch_norm<float, true>(a, stream);
+  else if (dtype == 1)
+    launch_norm<f16, true>(a, stream);
+  else
+    launch_norm<bf16, true>(a, stream);
+  return hipGetLastError();
+}
+
+int lb_norm_bwd_groups(int64_t rows, int64_t n) {
+  (void)n;
+  return (int)(rows < 512 ? rows : 512);
+}
+
+hipError_t lb_launch_norm_bwd(const LbNormBwdArgs& a, int dtype, hipStream_t stream) {
+  if (a.rows > 0) {
+    if (dtype == 1)
+      launch_bwd<f16>(a, stream);
+    else
+      launch_bwd<bf16>(a, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(lb_norm_dweight_kernel, dim3((a.n + 31) / 32), dim3(1024), 0, stream, a.partial, a.groups, a.n,
+                     a.dweight);
+  return hipGetLastError();
+}

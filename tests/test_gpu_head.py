@@ -1,0 +1,601 @@
+"""GPU parity of the dense operators around the LittleBit layers against the
+float64 reference (oracle/head.py).
+
+Bounds are counted in roundings.  u = 2^-24 is half a step of fp32, e = half a
+step of the output's type (eps / 2); sub is half its smallest subnormal.
+* A sum of N terms in fp32, however it is grouped, is off by at most
+  (longest chain of additions) * u * sum |terms|; a chain here is at most
+  the elements a thread holds, plus 6 in a wave, plus the waves and parts.
+* exp(d) from the hardware's base-2 exponential: d / ln 2 is rounded once, so
+  its value is off by |d| u, plus 2 u of the instruction: (|d| + 2) * 2 u.
+"""
+
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import head as oh
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TYPES = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+SUB = {torch.float32: 2.0 ** -150, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -134}
+
+
+@pytest.fixture(scope="module")
+def head():
+    from binary_rank_gemv_amd import head
+    return head
+
+
+def half_step(t):
+    return torch.finfo(t).eps / 2
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def rows_of(t, pad=0, offset=0):
+    """The same values in rows `pad` elements further apart, `offset` elements into their buffer."""
+    rows, n = t.shape
+    buf = torch.full((rows * (n + pad) + offset + pad,), 77, dtype=t.dtype, device="cuda")
+    v = buf[offset:offset + rows * (n + pad)].view(rows, n + pad)[:, :n]
+    v.copy_(t)
+    return v
+
+
+def randn(seed, *shape, scale=1.0):
+    return torch.from_numpy(np.random.default_rng(seed).standard_normal(shape) * scale)
+
+
+def case(*what):
+    print("[case]", *what, flush=True)
+
+
+# ----------------------------------------------------------------------------------------------------------- norm
+
+NORM_SHAPES = [(1, 1), (1, 7), (3, 8), (5, 100), (4, 512), (2, 513), (3, 2048), (2, 2056), (1, 4096), (1, 5120), (3, 8192),
+               (2, 8200), (1, 16384), (2, 16385), (1, 32768)]
+
+
+def chain(n):
+    return 32 + 6 + 16 + 4   # at most 32 elements a thread, 6 in a wave, 16 waves, sqrt / division / products
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,n", NORM_SHAPES)
+def test_norm_forward(head, rows, n, dt):
+    t = TYPES[dt]
+    for residual, pad, offset in ((True, 0, 0), (False, 3, 1), (True, 8, 5)):
+        case("norm", rows, n, dt, residual, pad, offset)
+        x, r = randn(n, rows, n).to(t), randn(n + 1, rows, n, scale=3.0).to(t)
+        w = (1 + 0.2 * randn(n + 2, n)).to(t)
+        xd, rd = rows_of(x, pad, offset), rows_of(r, pad, offset) if residual else None
+        q, scale, h1 = head.littlebit_rmsnorm_q8(xd, w.cuda(), rd)
+        y, h2 = head.littlebit_rmsnorm_fwd(xd, w.cuda(), rd)
+        torch.cuda.synchronize()
+        want_h = (x.double() + r.double()).to(t) if residual else x
+        assert torch.equal(h1.cpu(), want_h) and torch.equal(h2.cpu(), want_h)
+        want = oh.rmsnorm(f64(want_h), f64(w), 1e-5)
+        err = chain(n) * U
+        e = half_step(t)
+        assert (np.abs(f64(y) - want) <= (e + err * (1 + e)) * np.abs(want) + SUB[t]).all()
+        s = oh.q8_scale(want)
+        assert (np.abs(f64(scale) - s) <= err * s).all()
+        # a code is within half a step of the value, and one more step only where the value's own error reaches
+        codes = q.cpu().numpy().astype(np.float64)
+        assert np.abs(codes).max() <= 127 and (np.abs(codes).max(axis=1) == 127).all()
+        assert (np.abs(codes - want / s[:, None]) <= 0.5 + 127 * err).all()
+
+
+def test_norm_rows_of_zeros_nan_and_infinity(head):
+    case("norm special rows")
+    x = torch.ones(5, 300, dtype=torch.float16)
+    x[0] = 0
+    x[1, 7] = float("nan")
+    x[2, 299] = float("inf")
+    x[3] = 6e-8          # the smallest subnormal
+    q, scale, _ = head.littlebit_rmsnorm_q8(x.cuda(), torch.ones(300, dtype=torch.float16, device="cuda"), eps=0.0)
+    assert scale[1].isnan() and scale[2].isnan() and (q[1:3] == 0).all()
+    assert scale[0].isnan() and (q[0] == 0).all()     # 0 / sqrt(0): without eps a row of zeros has no norm
+    assert (q[3:] == 127).all() and torch.allclose(scale[3:], torch.tensor(1 / 127.0, device="cuda"), rtol=60 * U)
+    q, scale, _ = head.littlebit_rmsnorm_q8(x[:1].cuda(), torch.ones(300, dtype=torch.float16, device="cuda"))
+    assert scale[0] == 0 and (q == 0).all()
+    y, _ = head.littlebit_rmsnorm_fwd(x[1:3].cuda(), torch.ones(300, dtype=torch.float16, device="cuda"))
+    assert y[0].isnan().all() and y[1, 299].isnan() and (y[1, :299] == 0).all()
+    # an fp16 sum beyond the type's range is an infinity of the stored hidden state
+    big = torch.full((1, 8), 60000.0, dtype=torch.float16, device="cuda")
+    _, scale, h = head.littlebit_rmsnorm_q8(big, torch.ones(8, dtype=torch.float16, device="cuda"), big)
+    assert h.isinf().all() and scale.isnan().all()
+
+
+def test_norm_hidden_in_place_and_untouched_surroundings(head):
+    case("norm in place")
+    t = torch.bfloat16
+    x, r = randn(0, 9, 130).to(t), randn(1, 9, 130).to(t)
+    w = torch.ones(130, dtype=t, device="cuda")
+    for pick in (0, 1):
+        buf = torch.full((9 * 150 + 20,), 5.0, dtype=t, device="cuda")
+        views = [rows_of(x, 20), rows_of(r, 20)]
+        inner = buf[10:10 + 9 * 150].view(9, 150)[:, :130]
+        inner.copy_(views[pick])
+        views[pick] = inner
+        y, h = head.littlebit_rmsnorm_fwd(views[0], w, views[1], hidden=inner)
+        assert h.data_ptr() == inner.data_ptr()
+        assert torch.equal(inner.cpu(), (x.double() + r.double()).to(t))
+        outside = torch.ones_like(buf, dtype=torch.bool)
+        outside[10:10 + 9 * 150].view(9, 150)[:, :130] = False
+        assert (buf[outside] == 5).all()
+        assert torch.equal(y, head.littlebit_rmsnorm_fwd(x.cuda(), w, r.cuda())[0])
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,n", [(1, 1), (2, 7), (3, 100), (5, 2048), (700, 300), (1500, 64), (3, 4096), (2, 5000),
+                                    (2, 8192), (3, 9001), (2, 16384), (2, 32768)])
+def test_norm_backward(head, rows, n, dt):
+    t = TYPES[dt]
+    for with_dh, pad, offset in ((True, 0, 0), (False, 8, 0), (True, 5, 3)):
+        case("norm backward", rows, n, dt, with_dh, pad, offset)
+        h, dy, dh = (randn(n + i, rows, n, scale=s).to(t) for i, s in ((0, 2.0), (1, 0.5), (2, 0.5)))
+        w = (1 + 0.2 * randn(n + 3, n)).to(t)
+        dx, dw = head.littlebit_rmsnorm_bwd(rows_of(dy, pad, offset), rows_of(h, pad, offset), w.cuda(),
+                                            rows_of(dh, pad, offset) if with_dh else None)
+        torch.cuda.synchronize()
+        H, DY, W = f64(h), f64(dy), f64(w)
+        want_dx, want_dw = oh.rmsnorm_backward(DY, H, W, 1e-5, f64(dh) if with_dh else None)
+        r = 1 / np.sqrt((H * H).mean(1, keepdims=True) + 1e-5)
+        part = np.abs(H) * r ** 3 * np.mean(np.abs(W * DY * H), 1, keepdims=True)
+        size = r * np.abs(W * DY) + 2 * part + (np.abs(f64(dh)) if with_dh else 0)
+        err = (chain(n) + 8) * U * size
+        assert (np.abs(f64(dx) - want_dx) <= half_step(t) * (np.abs(want_dx) + err) + err + SUB[t]).all()
+        # dweight: a group's rows in turn, 32 slices of groups, 32 of those
+        terms = np.abs(DY * H * r).sum(0)
+        assert (np.abs(f64(dw) - want_dw) <= (rows + chain(n) + 64) * U * terms).all()
+
+
+def test_norm_backward_no_rows(head):
+    case("norm backward of no rows")
+    e = torch.empty(0, 50, dtype=torch.float16, device="cuda")
+    dx, dw = head.littlebit_rmsnorm_bwd(e, e, torch.ones(50, dtype=torch.float16, device="cuda"))
+    assert dx.shape == (0, 50) and (dw == 0).all()
+
+
+def test_norm_backward_repeats_bit_for_bit(head):
+    case("norm backward twice")
+    h, dy = randn(0, 3000, 520).bfloat16().cuda(), randn(1, 3000, 520).bfloat16().cuda()
+    w = torch.ones(520, dtype=torch.bfloat16, device="cuda")
+    a = head.littlebit_rmsnorm_bwd(dy, h, w)
+    b = head.littlebit_rmsnorm_bwd(dy, h, w)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ------------------------------------------------------------------------------------------------------- quantiser
+
+@pytest.mark.parametrize("dt", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("rows,n", [(1, 1), (3, 5), (2, 512), (3, 1000), (2, 4100), (1, 8192), (2, 20000)])
+def test_quantize(head, rows, n, dt):
+    t = TYPES[dt]
+    for pad, offset in ((0, 0), (3, 1)):
+        case("quantize", rows, n, dt, pad, offset)
+        x = randn(n, rows, n).to(t)
+        q, scale = head.littlebit_q8_quantize(rows_of(x, pad, offset))
+        s = oh.q8_scale(f64(x))
+        assert (np.abs(f64(scale) - s) <= U * s).all()
+        # 127 / max and the product with it: two roundings
+        assert (np.abs(f64(q) - f64(x) / s[:, None]) <= 0.5 + 127 * 3 * U).all()
+
+
+def test_quantize_ends_of_the_range(head):
+    case("quantize special rows")
+    x = torch.zeros(6, 40)
+    x[1] = 1e-38 * torch.arange(40)
+    x[2, 3] = float("inf")
+    x[3, 39] = float("nan")
+    x[4] = 3e38
+    x[5] = -1e-45
+    q, scale = head.littlebit_q8_quantize(x.cuda())
+    assert scale[0] == 0 and (q[0] == 0).all()
+    want = torch.round(x[1].double() / x[1].double().max() * 127)
+    assert (q[1].cpu().double() - want).abs().max() <= 1
+    assert scale[2].isnan() and scale[3].isnan() and (q[2:4] == 0).all()
+    assert (q[4] == 127).all() and torch.isfinite(scale[4])
+    assert (q[5] == -127).all()
+
+
+# ------------------------------------------------------------------------------------------------------ 8-bit product
+
+LINEAR = [(1, 1, 1), (1, 16, 64), (2, 17, 65), (3, 100, 128), (16, 33, 1000), (17, 64, 256), (31, 130, 320), (64, 48, 2048),
+          (65, 129, 512), (100, 200, 511), (128, 256, 1024), (130, 300, 640), (257, 513, 192), (300, 1000, 4096),
+          (520, 768, 128), (1, 4096, 13824), (5, 32000, 320)]
+
+
+@pytest.mark.parametrize("batch,m,n", LINEAR)
+def test_q8_linear(head, batch, m, n):
+    rng = np.random.default_rng(batch + m + n)
+    xq = torch.from_numpy(rng.integers(-128, 128, (batch, n), dtype=np.int8))
+    wq = torch.from_numpy(rng.integers(-128, 128, (m, n), dtype=np.int8))
+    xs = torch.from_numpy(rng.uniform(0.01, 0.1, batch).astype(np.float32))
+    ws = torch.from_numpy((rng.uniform(0.5, 1.5, m) / (60 * np.sqrt(n))).astype(np.float32))
+    want = oh.q8_linear(xq.numpy(), xs.numpy(), wq.numpy(), ws.numpy())
+    for dt, (pad, offset) in itertools.product(TYPES, ((0, 0), (16, 16), (3, 1))):
+        case("q8 linear", batch, m, n, dt, pad, offset)
+        t = TYPES[dt]
+        buf = torch.full((batch * (m + pad) + 2 * pad,), 9.0, dtype=t, device="cuda")
+        out = buf[pad:pad + batch * (m + pad)].view(batch, m + pad)[:, :m]
+        got = head.littlebit_q8_linear_fwd(rows_of(xq, pad, offset), xs.cuda(), rows_of(wq, pad, offset), ws.cuda(),
+                                           out=out)
+        torch.cuda.synchronize()
+        # the sum as fp32, the scales' product, their product, the output
+        assert (np.abs(f64(got) - want) <= (3 * U + half_step(t) * (1 + 4 * U)) * np.abs(want) + SUB[t]).all()
+        outside = torch.ones_like(buf, dtype=torch.bool)
+        outside[pad:pad + batch * (m + pad)].view(batch, m + pad)[:, :m] = False
+        assert (buf[outside] == 9).all()
+
+
+def test_q8_linear_at_the_largest_sum(head):
+    case("q8 linear, largest sums")
+    n = 131071
+    x = torch.full((2, n), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((3, n), -128, dtype=torch.int8, device="cuda")
+    w[1] = 127
+    one = torch.ones(3, device="cuda")
+    y = head.littlebit_q8_linear_fwd(x, one[:2], w, one, dtype=torch.float32)
+    want = torch.tensor([128.0 * 128 * n, -128.0 * 127 * n, 128.0 * 128 * n], dtype=torch.float64).float()
+    assert (y.cpu() == want).all()
+
+
+def test_q8_linear_codes_of_other_rows_do_not_reach_a_row(head):
+    """A padded batch: each token's output depends on its own codes alone."""
+    case("q8 linear rows")
+    rng = np.random.default_rng(0)
+    xq = torch.from_numpy(rng.integers(-127, 128, (150, 512), dtype=np.int8)).cuda()
+    wq = torch.from_numpy(rng.integers(-127, 128, (200, 512), dtype=np.int8)).cuda()
+    xs, ws = torch.rand(150, device="cuda"), torch.rand(200, device="cuda")
+    xs[7] = float("nan")
+    y = head.littlebit_q8_linear_fwd(xq, xs, wq, ws, dtype=torch.float32)
+    for t in (0, 6, 8, 149):
+        one = head.littlebit_q8_linear_fwd(xq[t:t + 1], xs[t:t + 1], wq, ws, dtype=torch.float32)
+        assert torch.equal(one[0], y[t])
+    assert y[7].isnan().all()
+
+
+# --------------------------------------------------------------------------------------------------- log probabilities
+
+def check_logprobs(head, x, targets, top, what, pad=0, offset=0):
+    """x: CPU tensor of logits."""
+    case("logprobs", what, tuple(x.shape), x.dtype, top, pad, offset)
+    xd = rows_of(x, pad, offset)
+    lp, H, parts, tv, ti = head.littlebit_logprobs_fwd(xd, targets.cuda(), top)
+    torch.cuda.synchronize()
+    lse = parts.sum(0)
+    X = f64(x)
+    logp, wantH = oh.logprobs(X)
+    want_lse = oh.logsumexp(X)
+    fine = np.isfinite(want_lse)
+    p = np.exp(logp)
+    far = np.where(p > 0, np.abs(np.where(p > 0, X, 0) - np.where(fine, X.max(1), 0)[:, None]), 0)
+    mean_far = (p * far).sum(1)
+    # chain of additions of a thread, a wave, the waves, the parts, and of a move to a new maximum a chunk
+    n = x.shape[1] / 256 + 16 + 6 + 4 + 32 + 2 * (x.shape[1] / 4096 + 1)
+    rel = (n + 4 + 2 * mean_far) * U                      # of the sum of exponentials
+    wl = np.where(fine, want_lse, 0)
+    tol = 2 * rel + 4 * U * (np.abs(wl) + np.abs(np.where(fine, X.max(1), 0))) + 8 * U
+    assert (np.abs(f64(lse) - wl)[fine] <= tol[fine]).all()
+    assert (np.isneginf(f64(lse)) == np.isneginf(want_lse)).all()
+    tolH = 2 * rel * (1 + 2 * mean_far) + 8 * U * (1 + wantH)
+    assert (np.abs(f64(H) - wantH) <= tolH).all()
+    tg = targets.numpy()
+    for i in range(len(tg)):
+        if tg[i] < 0:
+            assert lp[i] == 0
+        else:
+            want = logp[i, tg[i]]
+            assert (f64(lp[i]) == want if np.isneginf(want) else abs(f64(lp[i]) - want) <= tol[i] + 2 * U * abs(want))
+    if top:
+        places = oh.top(X, top)
+        assert np.array_equal(ti.cpu().numpy(), places)
+        want = np.take_along_axis(logp, places, 1)
+        got = f64(tv)
+        inf = np.isneginf(want)
+        assert (np.isneginf(got) == inf).all()
+        assert (np.abs(got - np.where(inf, 0, want))[~inf] <= (tol[:, None] + 2 * U * np.abs(np.where(inf, 0, want)))[~inf]).all()
+    else:
+        assert tv is None and ti is None
+    return xd, lp, H, parts, tv, ti
+
+
+def targets_of(seed, rows, vocab):
+    t = torch.from_numpy(np.random.default_rng(seed).integers(0, vocab, rows))
+    t[::5] = -100
+    return t
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("rows,vocab,top", [(1, 1, 1), (3, 2, 2), (4, 17, 17), (2, 64, 64), (5, 1000, 3), (2, 4096, 64),
+                                            (3, 4097, 20), (1, 8191, 1), (7, 12345, 33), (2, 32000, 5), (1, 100003, 64),
+                                            (600, 5000, 7), (1030, 300, 2), (3, 32000, 0)])
+def test_logprobs(head, rows, vocab, top, dt):
+    for pad, offset in ((0, 0), (3, 1)):
+        x = randn(vocab + rows, rows, vocab, scale=3.0).to(TYPES[dt])
+        check_logprobs(head, x, targets_of(rows, rows, vocab), top, "random", pad, offset)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("kind", ["equal", "few values", "rising", "falling", "masked", "one left", "nothing left",
+                                  "lowest", "far apart", "zeros of both signs", "peak"])
+def test_logprobs_hard_rows(head, kind, dt):
+    t, vocab, top = TYPES[dt], 9001, 20
+    low = torch.finfo(t).min
+    rng = np.random.default_rng(5)
+    x = randn(9, 3, vocab, scale=2.0)
+    if kind == "equal":
+        x[:] = 1.25
+    elif kind == "few values":
+        x = torch.from_numpy(rng.integers(0, 3, (3, vocab)).astype(np.float64))
+    elif kind == "rising":
+        x = torch.linspace(-8, 8, vocab, dtype=torch.float64).repeat(3, 1)
+    elif kind == "falling":
+        x = torch.linspace(8, -8, vocab, dtype=torch.float64).repeat(3, 1)
+    elif kind == "masked":
+        x[:, ::2] = -np.inf
+        x[1, 5:] = -np.inf          # fewer left than are asked for
+    elif kind == "one left":
+        x[:] = -np.inf
+        x[0, 0] = x[1, 4096] = x[2, vocab - 1] = 3.0
+    elif kind == "nothing left":
+        x[1] = -np.inf
+    elif kind == "lowest":
+        x[:, 1:] = low
+        x[1] = low
+    elif kind == "far apart":
+        x *= 2000.0
+    elif kind == "zeros of both signs":
+        x[:] = 0.0
+        x[:, ::3] = -0.0
+    elif kind == "peak":
+        x[:, 77] = 60.0
+    check_logprobs(head, x.to(t), torch.tensor([4, 77, 9000]), top, kind)
+
+
+def test_logprobs_nan_and_infinity(head):
+    case("logprobs nan")
+    x = randn(1, 4, 5000).float()
+    x[0, 40] = float("nan")
+    x[0, 4500] = -float("nan")
+    x[1, 4999] = float("inf")
+    targets = torch.tensor([0, 1, 5000, 2])
+    lp, H, lse, tv, ti = head.littlebit_logprobs_fwd(x.cuda(), targets.cuda(), 4)
+    assert lp[:3].isnan().all() and H[:2].isnan().all() and lse.sum(0)[:2].isnan().all()
+    assert torch.isfinite(lp[3]) and torch.isfinite(H[2:]).all()
+    assert np.array_equal(ti.cpu().numpy(), oh.top(f64(x), 4))
+
+
+def test_logprobs_without_targets(head):
+    case("logprobs without targets")
+    x = randn(1, 4, 5000).half().cuda()
+    a = head.littlebit_logprobs_fwd(x, None, 3)
+    b = head.littlebit_logprobs_fwd(x, torch.zeros(4, dtype=torch.int64, device="cuda"), 3)
+    assert a[0] is None and all(torch.equal(p, q) for p, q in zip(a[1:], b[1:]))
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("rows,vocab,top", [(1, 1, 1), (3, 2, 0), (4, 17, 5), (5, 1000, 64), (2, 8192, 4), (3, 8193, 3),
+                                            (7, 20011, 0), (2, 50257, 20)])
+def test_logprobs_backward(head, rows, vocab, top, dt):
+    t = TYPES[dt]
+    rng = np.random.default_rng(rows + vocab)
+    for pad, offset, use in ((0, 0, "all"), (3, 1, "all"), (0, 0, "token"), (0, 0, "entropy")):
+        x = randn(vocab, rows, vocab, scale=2.0).to(t)
+        x[:, vocab // 2] = -np.inf if vocab > 2 else x[:, 0]
+        targets = targets_of(rows, rows, vocab)
+        xd, lp, H, lse, tv, ti = check_logprobs(head, x, targets, top, use, pad, offset)
+        if top and use == "all":
+            targets = torch.where(targets >= 0, ti[:, 0].cpu(), targets)       # the target is an alternative too
+        g = torch.from_numpy(rng.standard_normal((2, rows)).astype(np.float32)).cuda()
+        gt = torch.from_numpy(rng.standard_normal((rows, top)).astype(np.float32)).cuda() if top and use == "all" else None
+        dlp, dH = (g[0] if use != "entropy" else None), (g[1] if use != "token" else None)
+        case("logprobs backward", rows, vocab, top, dt, pad, use)
+        d = head.littlebit_logprobs_bwd(xd, targets.cuda(), lse, H, dlp, dH, ti if gt is not None else None, gt)
+        torch.cuda.synchronize()
+        X = f64(x)
+        want = oh.logprobs_backward(X, targets.numpy(), f64(dlp) if dlp is not None else None,
+                                    f64(dH) if dH is not None else None, ti.cpu().numpy() if gt is not None else None,
+                                    f64(gt) if gt is not None else None)
+        logp, ent = oh.logprobs(X)
+        p = np.exp(logp)
+        y = np.where(p > 0, logp, 0)
+        a = (np.abs(f64(dlp))[:, None] if dlp is not None else 0) + (np.abs(f64(gt)).sum(1, keepdims=True) if gt is not None else 0)
+        b = np.abs(f64(dH))[:, None] if dH is not None else 0
+        # lse and H are off as in the forward test: 3e-5 of 1 covers vocab / 256 additions of 50257; exp as above
+        off = (vocab / 256 + 100) * U + 4 * U * (np.abs(y) + np.abs(np.where(p > 0, X, 0)) + np.abs(oh.logsumexp(X))[:, None])
+        err = p * (2 * off * (a + b * (np.abs(y) + ent[:, None])) + b * (off * 8 * (1 + ent[:, None])) + 70 * U * a)
+        err = err + 70 * U * (np.abs(want) + a * (p > 0))
+        assert (np.abs(f64(d) - want) <= half_step(t) * (np.abs(want) + err) + err + SUB[t]).all()
+        # in place, the same bits
+        head.littlebit_logprobs_bwd(xd, targets.cuda(), lse, H, dlp, dH, ti if gt is not None else None, gt, out=xd)
+        assert torch.equal(xd.cpu(), d.cpu())
+
+
+def test_logprobs_backward_special_rows(head):
+    case("logprobs backward special rows")
+    x = randn(2, 4, 700).float()
+    x[0] = -np.inf
+    x[1, 3] = -np.inf
+    targets = torch.tensor([2, 3, -100, 700]).cuda()
+    lp, H, lse, tv, ti = head.littlebit_logprobs_fwd(x.cuda(), targets, 2)
+    one = torch.ones(4, device="cuda")
+    d = head.littlebit_logprobs_bwd(x.cuda(), targets, lse, H, one, None, ti, torch.zeros(4, 2, device="cuda"))
+    assert (d[0] == 0).all()                       # nothing left: no gradient
+    assert d[1, 3] == 1 and lp[1] == -np.inf       # a masked token: its own direct gradient, p is 0
+    assert (d[2] == 0).all() and d[3].isnan().all()
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_logprobs_backward_of_rows_masked_with_the_lowest_value(head, dt):
+    """Equals, however far from 0: p is 1 / vocab everywhere, exact but for exp and log (8 U each)."""
+    case("logprobs backward, lowest", dt)
+    t = TYPES[dt]
+    x = torch.full((2, 1000), torch.finfo(t).min, dtype=t)
+    x[1, 7] = 0.0
+    targets = torch.tensor([3, 7]).cuda()
+    lp, H, lse, _, _ = head.littlebit_logprobs_fwd(x.cuda(), targets)
+    d = head.littlebit_logprobs_bwd(x.cuda(), targets, lse, H, torch.ones(2, device="cuda"), torch.ones(2, device="cuda"))
+    want = -torch.full((1000,), 1e-3, dtype=torch.float64)
+    want[3] += 1
+    assert ((d[0].cpu().double() - want).abs() <= (half_step(t) + 40 * U) * want.abs() + 40 * U * 1e-3 + SUB[t]).all()
+    assert (d[1] == 0).all() and lp[1] == 0 and H[1] == 0
+    assert abs(lp[0].item() + np.log(1000)) <= 8 * U * 7 and abs(H[0].item() - np.log(1000)) <= 40 * U * 7
+
+
+# ------------------------------------------------------------------------------------------------------- together
+
+def _model(head, n=512, vocab=2000, seed=3):
+    rng = np.random.default_rng(seed)
+    W = torch.from_numpy((rng.standard_normal((vocab, n)) / np.sqrt(n)).astype(np.float32)).cuda()
+    norm = torch.from_numpy(rng.uniform(0.5, 1.5, n)).half().cuda()
+    return W, norm, head.LittleBitHead.from_weights(norm, W)
+
+
+def test_block_to_token_probabilities(head):
+    """A LittleBit layer behind a norm, then the head: every operator as it is used,
+    against the float64 formulas on the same stored intermediates."""
+    case("layer, norm, head, log probabilities")
+    import oracle
+    from binary_rank_gemv_amd import littlebit as lb
+    from binary_rank_gemv_amd import synth
+    branches, x = synth.make_layer(synth.TINY, batch=6, seed=1)
+    layer = lb.LittleBitLayer.from_latents(branches)
+    W, norm, hd = _model(head)
+    x0 = torch.from_numpy(x).cuda()
+    res = torch.from_numpy(np.random.default_rng(2).standard_normal((6, 512))).half().cuda()
+    y, h = head.littlebit_rmsnorm_fwd(x0, norm, res)
+    z = lb.littlebit_linear_fwd(layer, y)
+    want_z = oracle.linear_forward(f64(y).astype(np.float16), branches)
+    assert np.linalg.norm(f64(z) - want_z) / np.linalg.norm(want_z) <= 2e-3
+    z = (z.float() / z.float().std()).half()
+    targets = torch.tensor([0, 1999, -100, 5, 6, 7]).cuda()
+    lp, H, tv, ti = hd.logprobs(z, targets, h, top=3)
+    # the same in float64 from the stored codes
+    hh = (z.double() + h.double()).half()
+    q, scale, h2 = head.littlebit_rmsnorm_q8(z, norm, h)
+    assert torch.equal(h2, hh)
+    vals = f64(q) * f64(scale)[:, None]
+    want_y = oh.rmsnorm(f64(hh), f64(norm), 1e-5)
+    assert np.abs(vals - want_y).max() <= oh.q8_scale(want_y).max() * 0.51
+    logits = oh.q8_linear(q.cpu().numpy(), f64(scale), hd.linear.q.cpu().numpy(), f64(hd.linear.scale))
+    logp, ent = oh.logprobs(logits)
+    rows = np.arange(6)
+    given = np.array([0, 1, 3, 4, 5])
+    assert np.abs(f64(lp)[given] - logp[rows, targets.cpu().numpy()][given]).max() <= 2e-5 and lp[2] == 0
+    assert np.abs(f64(H) - ent).max() <= 2e-5
+    # and 8 bits against the dense head: each factor's codes are within half a step of its largest value / 127,
+    # independent over the 512 inputs: their sum stays within six standard deviations
+    dense = want_y @ f64(W).T
+    sw, sx = oh.q8_scale(f64(W))[None, :], oh.q8_scale(want_y)[:, None]
+    dev = np.sqrt(((want_y ** 2).sum(1)[:, None] * sw ** 2 + (f64(W) ** 2).sum(1)[None, :] * sx ** 2) / 12)
+    assert (np.abs(logits - dense) <= 6 * dev).all()
+
+
+def test_head_text_in_parts_is_the_text_at_once(head):
+    case("head in parts")
+    W, norm, hd = _model(head)
+    x = randn(4, 75, 512).half().cuda()
+    targets = targets_of(1, 75, 2000).cuda()
+    whole = hd.logprobs(x, targets, top=2)
+    parts = hd.logprobs(x, targets, top=2, max_logit_bytes=2000 * 4 * 16)
+    for a, b in zip(whole, parts):
+        assert a.shape == b.shape and (torch.equal(a, b) if a.dtype == torch.int64 else torch.allclose(a, b, rtol=0, atol=1e-5))
+    e = hd.logprobs(x[:0], targets[:0], top=2)
+    assert e[0].shape == (0,) and e[3].shape == (0, 2)
+
+
+def test_streams_and_graphs(head):
+    """The chain captured once and replayed over new inputs, with the program's own
+    eager work between the replays; two graphs share nothing."""
+    case("graphs")
+    W, norm, hd = _model(head, vocab=9000)
+    lib_in = [torch.empty(3, 512, dtype=torch.float16, device="cuda") for _ in range(2)]
+    targets = torch.tensor([5, 8999, -1]).cuda()
+
+    def step(x):
+        logits = hd.logits(x)
+        lp, H, lse, tv, ti = head.littlebit_logprobs_fwd(logits, targets, 4)
+        d = head.littlebit_logprobs_bwd(logits, targets, lse, H, torch.ones(3, device="cuda"), torch.ones(3, device="cuda"),
+                                        ti, torch.ones(3, 4, device="cuda"))
+        y, h = head.littlebit_rmsnorm_fwd(x, norm, x)
+        dx, dw = head.littlebit_rmsnorm_bwd(y, h, norm)
+        return [logits, lp, H, lse, tv, ti, d, dx, dw]
+
+    graphs, outs = [], []
+    s = torch.cuda.Stream()
+    for x in lib_in:
+        x.normal_()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            step(x)
+        torch.cuda.current_stream().wait_stream(s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(step(x))
+        graphs.append(g)
+    for k in range(4):
+        for i, x in enumerate(lib_in):
+            x.copy_(randn(10 * k + i, 3, 512).half())
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for x, got in zip(lib_in, outs):
+            want = step(x)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # an explicit stream
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda.synchronize()
+    s.wait_stream(torch.cuda.current_stream())
+    q, scale, _ = head.littlebit_rmsnorm_q8(lib_in[0], norm, stream=s)
+    y = head.littlebit_q8_linear_fwd(q, scale, hd.linear.q, hd.linear.scale, dtype=torch.float32, stream=s)
+    s.synchronize()
+    assert torch.equal(y, outs[0][0])
+
+
+def test_refusals(head):
+    case("refusals")
+    x = torch.zeros(4, 64, dtype=torch.float16, device="cuda")
+    w = x[0]
+    f = torch.zeros(4, device="cuda")
+    q = torch.zeros(4, 64, dtype=torch.int8, device="cuda")
+    ti = torch.zeros(4, 2, dtype=torch.int64, device="cuda")
+    lse = torch.zeros(2, 4, device="cuda")
+    from binary_rank_gemv_amd.littlebit import LittleBitError
+    for call in (lambda: head.littlebit_rmsnorm_q8(x.t(), w[:4]),
+                 lambda: head.littlebit_rmsnorm_q8(x, w[:63]),
+                 lambda: head.littlebit_rmsnorm_q8(x, w.bfloat16()),
+                 lambda: head.littlebit_rmsnorm_q8(x, w, x[:3]),
+                 lambda: head.littlebit_rmsnorm_q8(x, w, hidden=x),
+                 lambda: head.littlebit_rmsnorm_q8(x[:1].expand(4, 64), w),
+                 lambda: head.littlebit_rmsnorm_q8(x.cpu(), w),
+                 lambda: head.littlebit_rmsnorm_bwd(x, x, w, x.float()),
+                 lambda: head.littlebit_q8_linear_fwd(q, f, q[:, :32], f),
+                 lambda: head.littlebit_q8_linear_fwd(q, f[:3], q, f),
+                 lambda: head.littlebit_q8_linear_fwd(q, f, q, f, dtype=torch.int32),
+                 lambda: head.littlebit_q8_linear_fwd(q, f, q, f, out=x),
+                 lambda: head.littlebit_logprobs_fwd(x, ti[:, 0]),
+                 lambda: head.littlebit_logprobs_fwd(x, f),
+                 lambda: head.littlebit_logprobs_bwd(x, None, f),
+                 lambda: head.littlebit_logprobs_bwd(x, None, lse, dlogprob=f),
+                 lambda: head.littlebit_logprobs_bwd(x, None, lse, dtop=f.view(4, 1)),
+                 lambda: head.littlebit_logprobs_bwd(x, None, lse, top_index=ti, dtop=torch.zeros(4, 3, device="cuda")),
+                 lambda: head.littlebit_logprobs_bwd(x, None, lse, dentropy=f)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: head.littlebit_logprobs_fwd(x, None, 65), lambda: head.littlebit_logprobs_fwd(x, None, -1),
+                 lambda: head.littlebit_rmsnorm_q8(x, w, eps=-1.0)):
+        with pytest.raises(LittleBitError):
+            call()
