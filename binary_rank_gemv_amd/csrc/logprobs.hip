@@ -8,11 +8,13 @@
 // several workgroups, whose parts a second kernel joins.
 //
 // Alternatives: a logit and its place make one 64-bit key (order of the value,
-// then the lower place), so no two are equal and the order is total.  Each
-// wave holds its 64 largest keys so far, lane i the i-th; only logits above
-// the top-th of them are looked at (a comparison of the thread's maximum of
-// 16 against it), are collected in LDS and, 64 at a time, sorted and merged
-// in.
+// then the lower place), so no two are equal and the order is total.  The pass
+// keeps each thread's maximum, nothing else.  The threads of equal lane are a
+// group; the top-th largest of the 64 groups' maxima is a bound that at
+// least `top` logits reach and few others do (24 expected for top 20, in a row
+// without ties), so only threads whose maximum reaches it read their part of
+// the row again and collect what reaches it in LDS, where the keys are
+// sorted, 64 at a time, over the lanes.
 #include "head_common.h"
 #include "head_launch.h"
 
@@ -21,12 +23,15 @@ using namespace lbh;
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
 constexpr int kEpt = 16;                    // elements a thread holds of a chunk
 constexpr int kChunk = kThreads * kEpt;     // 4096
 constexpr float kLow = -3.402823466e+38f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFar = -1e30f;              // below any distance whose exp is not 0
 constexpr int kBuf = 128;                   // collected keys a wave (64 merged at a time)
+constexpr int kKept = 8;                    // groups of chunks whose maxima a thread keeps for the second look
+constexpr int kWork = 256;                  // entries of the second look's list
 
 typedef unsigned long long u64;
 
@@ -38,6 +43,10 @@ __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f
 struct Stat {
   float m, s, e;
 };
+struct Part {
+  Stat s;
+  float xt;  // the target's logit, in the part that holds it
+};
 __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   Stat r;
   r.m = max_nan(a.m, b.m);
@@ -47,16 +56,21 @@ __device__ __forceinline__ Stat join(const Stat& a, const Stat& b) {
   r.e = (a.e + da * a.s) * ea + (b.e + db * b.s) * eb;
   return r;
 }
+template <int M>
+__device__ __forceinline__ Stat join_lane(const Stat& a) {
+  Stat b;
+  b.m = lane_xor<M>(a.m);
+  b.s = lane_xor<M>(a.s);
+  b.e = lane_xor<M>(a.e);
+  return join(a, b);
+}
 __device__ __forceinline__ Stat wave_join(Stat a) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    Stat b;
-    b.m = __shfl_xor(a.m, m, 64);
-    b.s = __shfl_xor(a.s, m, 64);
-    b.e = __shfl_xor(a.e, m, 64);
-    a = join(a, b);
-  }
-  return a;
+  a = join_lane<1>(a);
+  a = join_lane<2>(a);
+  a = join_lane<4>(a);
+  a = join_lane<8>(a);
+  a = join_lane<16>(a);
+  return join_lane<32>(a);
 }
 
 // ---------------------------------------------------------------- ordered keys
@@ -71,38 +85,62 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 }
 __device__ __forceinline__ u64 key_of(float x, uint32_t place) { return (u64)order_of(x) << 32 | (uint32_t)~place; }
 
-__device__ __forceinline__ u64 shfl_xor64(u64 v, int m) {
-  const uint32_t lo = __shfl_xor((uint32_t)v, m, 64), hi = __shfl_xor((uint32_t)(v >> 32), m, 64);
-  return (u64)hi << 32 | lo;
+template <int M>
+__device__ __forceinline__ uint32_t other(uint32_t v) { return lane_xor<M>(v); }
+template <int M>
+__device__ __forceinline__ u64 other(u64 v) {
+  return (u64)lane_xor<M>((uint32_t)(v >> 32)) << 32 | lane_xor<M>((uint32_t)v);
 }
-__device__ __forceinline__ u64 lane64(u64 v, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane);
-  const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
-  return (u64)hi << 32 | lo;
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ u64 lane_of(u64 v, int lane) {
+  return (u64)lane_of((uint32_t)(v >> 32), lane) << 32 | lane_of((uint32_t)v, lane);
 }
 
-// One exchange of a bitonic network: the lane whose bit `m` is clear keeps the
-// larger key if `down`, the smaller otherwise.
-__device__ __forceinline__ u64 exchange(u64 v, int m, bool down, int lane) {
-  const u64 o = shfl_xor64(v, m);
-  const bool keep_larger = ((lane & m) == 0) == down;
+// One exchange of a bitonic network over the lanes: the lane whose bit M is
+// clear keeps the larger key if `down`, the smaller otherwise.
+template <int M, typename K>
+__device__ __forceinline__ K exchange(K v, bool down, int lane) {
+  const K o = other<M>(v);
+  const bool keep_larger = ((lane & M) == 0) == down;
   return (v > o) == keep_larger ? v : o;
 }
-__device__ inline u64 sort64(u64 v, int lane) {  // lane 0 the largest
-#pragma unroll
-  for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-    for (int m = k >> 1; m > 0; m >>= 1) v = exchange(v, m, (lane & k) == 0, lane);
-  return v;
+template <typename K>
+__device__ __forceinline__ K falling64(K v, int lane) {  // of a bitonic sequence
+  v = exchange<32>(v, true, lane);
+  v = exchange<16>(v, true, lane);
+  v = exchange<8>(v, true, lane);
+  v = exchange<4>(v, true, lane);
+  v = exchange<2>(v, true, lane);
+  return exchange<1>(v, true, lane);
 }
-// The 64 largest of two sorted lists, sorted.
-__device__ inline u64 merge64(u64 a, u64 b, int lane) {
-  const uint32_t lo = __shfl((uint32_t)b, 63 - lane, 64), hi = __shfl((uint32_t)(b >> 32), 63 - lane, 64);
-  const u64 r = (u64)hi << 32 | lo;
-  u64 v = a > r ? a : r;
-#pragma unroll
-  for (int m = 32; m > 0; m >>= 1) v = exchange(v, m, true, lane);
-  return v;
+template <typename K>
+__device__ __forceinline__ K sort64(K v, int lane) {  // lane 0 the largest
+  bool d = (lane & 2) == 0;
+  v = exchange<1>(v, d, lane);
+  d = (lane & 4) == 0;
+  v = exchange<2>(v, d, lane);
+  v = exchange<1>(v, d, lane);
+  d = (lane & 8) == 0;
+  v = exchange<4>(v, d, lane);
+  v = exchange<2>(v, d, lane);
+  v = exchange<1>(v, d, lane);
+  d = (lane & 16) == 0;
+  v = exchange<8>(v, d, lane);
+  v = exchange<4>(v, d, lane);
+  v = exchange<2>(v, d, lane);
+  v = exchange<1>(v, d, lane);
+  d = (lane & 32) == 0;
+  v = exchange<16>(v, d, lane);
+  v = exchange<8>(v, d, lane);
+  v = exchange<4>(v, d, lane);
+  v = exchange<2>(v, d, lane);
+  v = exchange<1>(v, d, lane);
+  return falling64(v, lane);
+}
+// The 64 largest of two falling lists, falling.
+__device__ __forceinline__ u64 merge64(u64 a, u64 b, int lane) {
+  const u64 r = other<32>(other<16>(other<15>(b)));  // b backwards
+  return falling64(a > r ? a : r, lane);
 }
 
 // The wave's LDS accesses stand in program order (the hardware keeps a wave's
@@ -112,83 +150,57 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// A wave's largest keys: `list` sorted over the lanes (0 where there are fewer
+// A wave's largest keys: `list` falling over the lanes (0 where there are fewer
 // than 64), `pending` more in its part of LDS.
 struct Tops {
   u64 list;
+  u64 least;  // the top-th of the list: a key has to be larger (0: any)
   int pending;
-  float bar;  // value of the top-th key; NaN while there are fewer
 };
 
+// Moves `take` keys (at most 64) from the front of the buffer into the list.
 __device__ __forceinline__ void tops_flush(Tops& T, u64* buf, int top, int lane, int take) {
-  // `take` keys (at most 64) from the front; the rest moves up
-  u64 k = lane < take ? buf[lane] : 0;
+  const u64 k = lane < take ? buf[lane] : 0;
   const int rest = T.pending - take;
   const u64 moved = lane < rest ? buf[take + lane] : 0;
   wave_fence();
   if (lane < rest) buf[lane] = moved;
   wave_fence();
   T.pending = rest;
-  k = sort64(k, lane);
-  T.list = merge64(T.list, k, lane);
-  const u64 b = lane64(T.list, top - 1);
-  T.bar = b ? value_of((uint32_t)(b >> 32)) : NAN;
+  T.list = merge64(T.list, sort64(k, lane), lane);
+  T.least = lane_of(T.list, top - 1);
 }
 
-// Collects the chunk's logits that can be among the `top` largest.  `v` holds
-// kEpt of them, the first `valid` inside the row, `most` their maximum;
+// Collects the chunk's logits of at least `floor` (NaN: all) that can be among
+// the `top` largest.  `v` holds kEpt of them, the first `valid` inside the row;
 // place(i) is where the i-th stands.
 template <typename PLACE>
 __device__ __forceinline__ void tops_chunk(Tops& T, u64* buf, int top, int lane, const float (&v)[kEpt], int valid,
-                                           float most, PLACE place) {
-  // a chunk comes after all that is in the list, so an equal value is no better
-  const bool some = valid > 0 && !(most <= T.bar);
-  const u64 lanes = __ballot(some);
-  if (lanes == 0) return;
-  u64 least = 0;
-  if (__popcll(lanes) > 32) {
-    // many at once (the first chunk): the top-th of the lanes' own largest is a bar too
-    u64 mine = 0;
-#pragma unroll
-    for (int i = 0; i < kEpt; ++i)
-      if (i < valid) {
-        const u64 k = key_of(v[i], place(i));
-        mine = k > mine ? k : mine;
-      }
-    least = lane64(sort64(mine, lane), top - 1);
-  }
-  // places inside the chunk are in no order over the lanes, so what the list
-  // takes in meanwhile raises `least` (a whole key), not the bar on values
-  const float bar = T.bar;
-  const float floor = least ? value_of((uint32_t)(least >> 32)) : NAN;
+                                           float floor, PLACE place) {
   uint32_t todo = 0;
 #pragma unroll
   for (int i = 0; i < kEpt; ++i)
-    if (i < valid && !(v[i] <= bar) && !(v[i] < floor)) todo |= 1u << i;
-  u64 rest;
-  while ((rest = __ballot(todo != 0)) != 0) {
+    if (i < valid && !(v[i] < floor)) todo |= 1u << i;
+  while (__ballot(todo != 0) != 0) {
     const int i = todo ? __builtin_ctz(todo) : 0;
-    todo &= todo - 1;
     float x = v[0];
 #pragma unroll
     for (int j = 1; j < kEpt; ++j) x = i == j ? v[j] : x;
     const u64 k = key_of(x, place(i));
-    const bool in = (rest >> lane & 1) && k >= least;
+    const bool in = todo && k > T.least;
     const u64 ins = __ballot(in);
     if (in) buf[T.pending + __popcll(ins & ((1ull << lane) - 1))] = k;
+    todo &= todo - 1;
     wave_fence();
     T.pending += __popcll(ins);
-    if (T.pending >= 64) {
-      tops_flush(T, buf, top, lane, 64);
-      const u64 b = lane64(T.list, top - 1);
-      least = b > least ? b : least;
-    }
+    if (T.pending >= 64) tops_flush(T, buf, top, lane, 64);
   }
 }
 
 // ------------------------------------------------------------------- the parts
-// What one workgroup leaves of its span of a row, when a row is split.
-__host__ __device__ inline size_t part_bytes(int top) { return 16 + 8 * (size_t)top; }
+// What one workgroup leaves of its span of a row, when a row is split: one
+// Part, and behind those of all rows `top` keys a part.
+__host__ __device__ inline size_t part_keys_at(long parts) { return (size_t)parts * sizeof(Part); }
 
 __device__ __forceinline__ void write_row(const LbLogprobsArgs& A, long row, const Stat& S, float xt, int64_t target) {
   const float logs = logf(S.s);
@@ -212,36 +224,86 @@ __device__ __forceinline__ void write_top(const LbLogprobsArgs& A, long row, con
   A.top_logprob[row * A.top + lane] = S.s == 0.0f ? (x != x ? x : -INFINITY) : (x - S.m) - logf(S.s);
 }
 
+// The 64 largest of `count` keys, falling, in wave 0; `keys` in LDS or global
+// memory, `room` LDS for the waves' lists.  Whole workgroup.
+__device__ __forceinline__ u64 block_top(const u64* keys, int count, u64 (*room)[64], int w, int lane) {
+  u64 list = 0;
+  for (int at = 64 * w; at < count; at += 64 * kWaves) {
+    u64 k = at + lane < count ? keys[at + lane] : 0;
+    if (count > 1) k = sort64(k, lane);
+    list = at == 64 * w ? k : merge64(list, k, lane);
+  }
+  if (count > 64) {
+    room[w][lane] = list;
+    __syncthreads();
+    if (w == 0) {
+      const int lists = min(kWaves, (count + 63) / 64);
+      for (int i = 1; i < lists; ++i) list = merge64(list, room[i][lane], lane);
+    }
+  }
+  return list;
+}
+
 template <typename T>
-__device__ __forceinline__ float target_logit(const LbLogprobsArgs& A, long row, int64_t target) {
-  if (target < 0 || target >= A.vocab) return 0.0f;
-  return (float)((const T*)A.logits)[row * A.ld + target];
+struct Chunk {
+  u32x4 w[kEpt * sizeof(T) / 16];
+};
+// 16-byte words of two vectors of eight; what lies behind the row is -infinity.
+template <typename T>
+__device__ __forceinline__ void chunk_load(Chunk<T>& C, const T* x, long c, long end, int t) {
+  constexpr int kW = sizeof(T) / 2;  // 16-byte words a vector
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const long k = c + 8 * (t + h * kThreads), left = end - k;
+    if (left >= 8) {
+#pragma unroll
+      for (int j = 0; j < kW; ++j) C.w[h * kW + j] = load_any<u32x4>((const char*)(x + k) + 16 * j);
+    } else {
+      T e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = i < left ? x[k + i] : (T)-INFINITY;
+      __builtin_memcpy(&C.w[h * kW], e, sizeof e);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void chunk_values(const Chunk<T>& C, float (&v)[kEpt]) {
+#pragma unroll
+  for (int i = 0; i < kEpt; ++i) {
+    if constexpr (sizeof(T) == 4)
+      v[i] = __builtin_bit_cast(float, (uint32_t)C.w[i >> 2][i & 3]);
+    else
+      v[i] = i & 1 ? Pair<T>::hi(C.w[i >> 3][(i >> 1) & 3]) : Pair<T>::lo(C.w[i >> 3][(i >> 1) & 3]);
+  }
 }
 
 template <typename T, bool TOP>
 __global__ __launch_bounds__(kThreads) void lb_logprobs_kernel(const LbLogprobsArgs A) {
-  constexpr int kWaves = kThreads / 64;
   __shared__ u64 buf[TOP ? kWaves : 1][kBuf];
+  __shared__ u64 keys[TOP ? kWaves * 64 : 1];
+  __shared__ uint32_t group[TOP ? kWaves : 1][64];
+  __shared__ float kept[TOP ? kKept : 1][TOP ? kThreads : 1];
+  __shared__ uint32_t work[TOP ? kWork : 1];
+  __shared__ int listed, counts[kWaves];
   __shared__ Stat stat[kWaves];
   const int t = threadIdx.x, w = wave_id(), lane = t & 63;
   const long row = blockIdx.x / A.splits;
   const int split = (int)(blockIdx.x - row * A.splits);
-  const int begin = split * A.span;
-  const int end = (int)min((long)A.vocab, (long)begin + A.span);
+  const long begin = (long)split * A.span;
+  const long end = min((long)A.vocab, begin + A.span);
   const T* x = (const T*)A.logits + row * A.ld;
+  const int64_t target = A.targets ? A.targets[row] : -1;
+  const float xt = target >= begin && target < end ? (float)x[target] : 0.0f;
   Stat S = {kLow, 0.0f, 0.0f};
-  Tops P = {0, 0, NAN};
+  float largest = -INFINITY;
+  const int per = (int)((end - begin + kKept * kChunk - 1) / (kKept * kChunk));  // chunks a kept maximum
+  int slot = 0, in_slot = 0;
+  Chunk<T> next;
+  chunk_load<T>(next, x, begin, end, t);
   for (long c = begin; c < end; c += kChunk) {
     float v[kEpt];
-    const long k0 = c + 8 * t, k1 = k0 + 8 * kThreads;
-    float lo[8], hi[8];
-    load8(x + k0, end - k0, -INFINITY, lo);
-    load8(x + k1, end - k1, -INFINITY, hi);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = lo[i];
-      v[8 + i] = hi[i];
-    }
+    chunk_values(next, v);
+    if (c + kChunk < end) chunk_load<T>(next, x, c + kChunk, end, t);
     float most = v[0];
 #pragma unroll
     for (int i = 1; i < kEpt; ++i) most = max_nan(most, v[i]);
@@ -259,66 +321,146 @@ __global__ __launch_bounds__(kThreads) void lb_logprobs_kernel(const LbLogprobsA
     S.s = s;
     S.e = e;
     if constexpr (TOP) {
-      const long left0 = end - k0, left1 = end - k1;
-      const int n0 = left0 >= 8 ? 8 : left0 > 0 ? (int)left0 : 0, n1 = left1 >= 8 ? 8 : left1 > 0 ? (int)left1 : 0;
-      const int valid = n1 > 0 ? 8 + n1 : n0;  // the first eight are whole where the second have any
-      tops_chunk(P, buf[w], A.top, lane, v, valid, most,
-                 [&](int i) { return (uint32_t)(i < 8 ? k0 + i : k1 + i - 8); });
+      largest = max_nan(largest, most);
+      kept[slot][t] = in_slot == 0 ? most : max_nan(kept[slot][t], most);  // this thread's alone
+      if (++in_slot == per) {
+        in_slot = 0;
+        ++slot;
+      }
     }
   }
   S = wave_join(S);
   if (lane == 0) stat[w] = S;
+  int count = 0;
   if constexpr (TOP) {
-    if (P.pending > 0) tops_flush(P, buf[w], A.top, lane, P.pending);
+    // (a thread without a part of the row counts for nothing)
+    const uint32_t mine = begin + 8 * t < end ? order_of(largest) : 0;
+    group[w][lane] = mine;
+    if (t == 0) listed = 0;
     __syncthreads();
-    buf[w][lane] = P.list;
+    uint32_t g = group[0][lane];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) g = max(g, group[i][lane]);
+    uint32_t bound;
+    if (A.top == 1) {
+      g = max(g, other<1>(g));
+      g = max(g, other<2>(g));
+      g = max(g, other<4>(g));
+      g = max(g, other<8>(g));
+      g = max(g, other<16>(g));
+      bound = lane_of(max(g, other<32>(g)), 0);
+    } else {
+      bound = lane_of(sort64(g, lane), A.top - 1);
+    }
+    const float floor = bound ? value_of(bound) : NAN;
+    Tops P = {0, 0, 0};
+    const bool any = mine && mine >= bound;
+    const int slots = (int)((end - begin + (long)per * kChunk - 1) / ((long)per * kChunk));
+    if (__ballot(any) != 0) {
+      u64 hit[kKept];
+      int hits = 0, at = 0;
+#pragma unroll
+      for (int j = 0; j < kKept; ++j) {
+        hit[j] = __ballot(any && j < slots && !(kept[j][t] < floor));
+        hits += __popcll(hit[j]);
+      }
+      if (lane == 0) at = atomicAdd(&listed, hits);
+      at = lane_of((uint32_t)at, 0);
+#pragma unroll
+      for (int j = 0; j < kKept; ++j) {
+        const int p = at + __popcll(hit[j] & ((1ull << lane) - 1));
+        if ((hit[j] >> lane & 1) && p < kWork) work[p] = (uint32_t)j << 16 | t;
+        at += __popcll(hit[j]);
+      }
+    }
+    __syncthreads();
+    const int entries = listed;
+    // a lane an entry; with more entries than the list takes (many equal
+    // logits) every thread looks through its own
+    const bool by_list = entries <= kWork;
+    const int entry = 64 * w + lane;
+    const uint32_t what = by_list ? (entry < entries ? work[entry] : 0) : t;
+    const int from = what & 0xFFFF;
+    const long first_c = begin + (long)(what >> 16) * per * kChunk;
+    const long last_c = by_list ? first_c + (long)per * kChunk : end;
+    const bool mine_too = by_list ? entry < entries : any;
+    if (__ballot(mine_too) != 0) {
+      const int rounds = by_list ? per : slots * per;
+      for (int i = 0; i < rounds; ++i) {
+        const long c = first_c + (long)i * kChunk;
+        const long stop = mine_too && c < last_c ? end : c;
+        const long k0 = c + 8 * from, k1 = k0 + 8 * kThreads;
+        const long left0 = stop - k0, left1 = stop - k1;
+        const int n0 = left0 >= 8 ? 8 : left0 > 0 ? (int)left0 : 0, n1 = left1 >= 8 ? 8 : left1 > 0 ? (int)left1 : 0;
+        const int valid = n1 > 0 ? 8 + n1 : n0;  // the first eight are whole where the second have any
+        float v[kEpt];
+        Chunk<T> part;
+        chunk_load<T>(part, x, c, stop, from);
+        chunk_values(part, v);
+        tops_chunk(P, buf[w], A.top, lane, v, valid, floor,
+                   [&](int i) { return (uint32_t)(i < 8 ? k0 + i : k1 + i - 8); });
+      }
+    }
+    // a wave that merged before brings the `top` first of its list, one that did not what it collected
+    const u64 first = lane_of(P.list, 0);
+    if (first && P.pending > 0) tops_flush(P, buf[w], A.top, lane, P.pending);
+    const int mine_n = first ? A.top : P.pending;
+    if (lane == 0) counts[w] = mine_n;
+    __syncthreads();
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      at += i < w ? counts[i] : 0;
+      count += counts[i];
+    }
+    if (lane < mine_n) keys[at + lane] = first ? P.list : buf[w][lane];
   }
   __syncthreads();
+  u64 list = 0;
+  if constexpr (TOP) list = block_top(keys, count, reinterpret_cast<u64(*)[64]>(&buf[0][0]), w, lane);
   if (w != 0) return;
-  S = stat[0];
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) S = join(S, stat[i]);
-  u64 list = P.list;
-  if constexpr (TOP) {
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) list = merge64(list, buf[i][lane], lane);
-  }
+  S = lane < kWaves ? stat[lane] : Stat{kLow, 0.0f, 0.0f};
+  S = join_lane<1>(S);
+  S = join_lane<2>(S);
+  S.m = __builtin_bit_cast(float, lane_of(__builtin_bit_cast(uint32_t, S.m), 0));
+  S.s = __builtin_bit_cast(float, lane_of(__builtin_bit_cast(uint32_t, S.s), 0));
+  S.e = __builtin_bit_cast(float, lane_of(__builtin_bit_cast(uint32_t, S.e), 0));
   if (A.splits == 1) {
-    if (lane == 0) {
-      const int64_t target = A.targets ? A.targets[row] : -1;
-      write_row(A, row, S, target_logit<T>(A, row, target), target);
-    }
+    if (lane == 0) write_row(A, row, S, xt, target);
     if constexpr (TOP) write_top(A, row, S, list, lane);
   } else {
-    char* part = (char*)A.ws + (size_t)blockIdx.x * part_bytes(A.top);
-    if (lane == 0) *(Stat*)part = S;
+    if (lane == 0) reinterpret_cast<Part*>(A.ws)[blockIdx.x] = Part{S, xt};
     if constexpr (TOP)
-      if (lane < A.top) ((u64*)(part + 16))[lane] = list;
+      if (lane < A.top)
+        reinterpret_cast<u64*>((char*)A.ws + part_keys_at(A.rows * A.splits))[(long)blockIdx.x * A.top + lane] = list;
   }
 }
 
-// Joins the parts of a row: one wave a row.
-template <typename T>
-__global__ __launch_bounds__(64) void lb_logprobs_join_kernel(const LbLogprobsArgs A) {
-  const int lane = threadIdx.x;
+// Joins the parts of a row.
+__global__ __launch_bounds__(kThreads) void lb_logprobs_join_kernel(const LbLogprobsArgs A) {
+  __shared__ u64 room[kWaves][64];
+  const int w = wave_id(), lane = threadIdx.x & 63;
   const long row = blockIdx.x;
-  const size_t bytes = part_bytes(A.top);
-  const char* parts = (const char*)A.ws + (size_t)row * A.splits * bytes;
+  const int64_t target = A.targets ? A.targets[row] : -1;
+  const Part* parts = reinterpret_cast<const Part*>(A.ws) + row * A.splits;
   Stat S = {kLow, 0.0f, 0.0f};
-  for (int i = lane; i < A.splits; i += 64) S = join(S, *(const Stat*)(parts + i * bytes));
-  S = wave_join(S);
+  float xt = 0.0f;
+  for (int i = lane; i < A.splits; i += 64) {
+    const Part p = parts[i];
+    S = join(S, p.s);
+    if (target >= (long)i * A.span && target < (long)(i + 1) * A.span) xt = p.xt;
+  }
+  u64 list = 0;
   if (A.top > 0) {
-    u64 list = lane < A.top ? ((const u64*)(parts + 16))[lane] : 0;
-    for (int i = 1; i < A.splits; ++i) {
-      const u64 k = lane < A.top ? ((const u64*)(parts + i * bytes + 16))[lane] : 0;
-      list = merge64(list, k, lane);
-    }
-    write_top(A, row, S, list, lane);
+    const u64* keys = reinterpret_cast<const u64*>((const char*)A.ws + part_keys_at(A.rows * A.splits));
+    list = block_top(keys + row * A.splits * A.top, A.splits * A.top, room, w, lane);
   }
-  if (lane == 0) {
-    const int64_t target = A.targets ? A.targets[row] : -1;
-    write_row(A, row, S, target_logit<T>(A, row, target), target);
-  }
+  if (w != 0) return;
+  S = wave_join(S);
+  const u64 owner = __ballot(xt != 0.0f);  // at most one lane (none where the logit is 0)
+  if (owner) xt = __builtin_bit_cast(float, lane_of(__builtin_bit_cast(uint32_t, xt), __builtin_ctzll(owner)));
+  if (A.top > 0) write_top(A, row, S, list, lane);
+  if (lane == 0) write_row(A, row, S, xt, target);
 }
 
 // -------------------------------------------------------------------- backward
@@ -399,8 +541,7 @@ void launch_fwd(const LbLogprobsArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((lb_logprobs_kernel<T, true>), grid, dim3(kThreads), 0, stream, a);
   else
     hipLaunchKernelGGL((lb_logprobs_kernel<T, false>), grid, dim3(kThreads), 0, stream, a);
-  if (a.splits > 1)
-    hipLaunchKernelGGL((lb_logprobs_join_kernel<T>), dim3((unsigned)a.rows), dim3(64), 0, stream, a);
+  if (a.splits > 1) hipLaunchKernelGGL(lb_logprobs_join_kernel, dim3((unsigned)a.rows), dim3(kThreads), 0, stream, a);
 }
 
 template <typename T>
@@ -411,21 +552,30 @@ void launch_bwd(const LbLogprobsBwdArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Workgroups a row: one where the rows alone fill the card, else as many as
-// give about 1024 workgroups, each with a whole chunk at least.
+// Workgroups a row.  A row of up to 16 chunks is one workgroup's: splitting it
+// saves 3 to 4 us on the card (17 x 50257 fp32 with 4 alternatives: 13.3 us
+// whole, 10.3 in 8 parts; 128 x 32000 fp16: 10.8 whole, 12.1 in 2), which the
+// second launch and its workspace cost on the host.  A longer one is split
+// into parts of two chunks at least while the card has fewer than 512
+// workgroups (1 x 128256 bf16 with 5 alternatives: 26.8 us whole, 10.9 in 8;
+// 61 x 100003 with 20: 23.9 and 14.4; 512 x 128256: 37.8, and 35.5 in 2).
 int lb_logprobs_splits(int64_t rows, int64_t vocab, int dtype, int* span) {
   (void)dtype;
   const int64_t chunks = (vocab + kChunk - 1) / kChunk;
-  int64_t splits = rows > 0 ? 1024 / rows : 1;
-  if (splits > chunks) splits = chunks;
+  int64_t splits = rows > 0 && chunks > 16 ? 512 / rows : 1;
+  if (splits > (chunks + 1) / 2) splits = (chunks + 1) / 2;
   if (splits < 1) splits = 1;
   const int64_t per = (chunks + splits - 1) / splits;
-  *span = (int)(per * kChunk < vocab ? per * kChunk : (vocab + 7) / 8 * 8);
+  if (per >= chunks) {
+    *span = (int)((vocab + 7) / 8 * 8);
+    return 1;
+  }
+  *span = (int)(per * kChunk);
   return (int)((chunks + per - 1) / per);
 }
 
 size_t lb_logprobs_partial_bytes(int64_t rows, int splits, int top) {
-  return splits > 1 ? (size_t)rows * splits * part_bytes(top) : 0;
+  return splits > 1 ? part_keys_at(rows * splits) + (size_t)rows * splits * top * sizeof(u64) : 0;
 }
 
 hipError_t lb_launch_logprobs(const LbLogprobsArgs& a, int dtype, hipStream_t stream) {

@@ -47,6 +47,7 @@ HEAD_EXPORTED = (
 
 _DTYPE = {torch.float32: LB_F32, torch.float16: LB_F16, torch.bfloat16: LB_BF16}
 _HALF = {torch.float16: LB_F16, torch.bfloat16: LB_BF16}
+_INT8 = {torch.int8: 0}
 
 
 def _load():
@@ -84,38 +85,53 @@ def _check(status: int):
 
 
 _HERE = contextlib.nullcontext()
+_empty = torch.empty_strided   # the cheapest way to an uninitialised tensor: these calls are short
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(t: torch.Tensor, stream):
-    """(context, stream pointer): the device of `t` current, allocations on `stream`."""
+def _on(device, stream):
+    """(context, stream pointer): `device` current, allocations on `stream`."""
     if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
         return torch.cuda.stream(stream), int(stream.cuda_stream)
-    index = t.device.index
-    here = torch.cuda.current_device()
-    return (_HERE if index == here else torch.cuda.device(index)), torch.cuda.current_stream(index).cuda_stream
+    index = device.index
+    return (_HERE if index == torch.cuda.current_device() else torch.cuda.device(index)), _raw_stream(index)
 
 
-def _matrix(name: str, t: torch.Tensor, dtype, device, shape=None):
-    """Checks a row-major matrix argument (unit column stride, any row stride)."""
+def _matrix(name: str, t: torch.Tensor, dtype, device, shape) -> int:
+    """Checks a row-major matrix argument (unit column stride, any row stride)
+    and returns its row stride; of a single row, at least its length."""
+    if torch.is_tensor(t) and t.dtype is dtype and t.device == device and t.shape == shape and device.type == "cuda":
+        rows, cols = shape
+        if t.is_contiguous():
+            return cols
+        if (cols == 1 or t.stride(1) == 1) and (rows == 1 or t.stride(0) >= cols):
+            return max(t.stride(0), cols)
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
     if not torch.is_tensor(t) or t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call is on {device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
-        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+
+
+def _first(name: str, t: torch.Tensor, dtypes):
+    """(dtype code, shape, device) of the argument that the others are held to."""
+    code = dtypes.get(t.dtype) if torch.is_tensor(t) else None
+    if code is None:
+        raise ValueError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    return code, t.shape, t.device
 
 
 def _vector(name: str, t: torch.Tensor, dtype, device, n: int):
-    if not torch.is_tensor(t) or t.dim() != 1 or not t.is_cuda or t.dtype != dtype or t.device != device:
+    if not torch.is_tensor(t) or t.dtype is not dtype or t.device != device or t.dim() != 1:
         raise ValueError(f"{name} must be a 1-D {dtype} tensor on {device}")
-    if t.shape[0] != n or n > 1 and t.stride(0) != 1:
+    if t.shape[0] != n or not t.is_contiguous():
         raise ValueError(f"{name} must be {n} contiguous values")
 
 
@@ -124,47 +140,47 @@ def _table(name: str, t: torch.Tensor, dtype, device, shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride; of a single row, whatever its stride says, at least its length."""
-    return max(t.stride(0), t.shape[1])
+def _new(rows: int, n: int, dtype, device) -> torch.Tensor:
+    return _empty((rows, n), (n, 1), dtype=dtype, device=device)
 
 
-def _codes(rows: int, n: int, device) -> torch.Tensor:
-    """Room for int8 codes, rows 16 bytes aligned (the product's fast case)."""
-    return torch.empty((rows, (n + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :n] if n % 16 else \
-        torch.empty((rows, n), dtype=torch.int8, device=device)
+def _codes(rows: int, n: int, device):
+    """Room for int8 codes and its row stride: rows 16 bytes aligned (the product's fast case)."""
+    ld = (n + 15) // 16 * 16
+    if ld == n:
+        return _new(rows, n, torch.int8, device), n
+    return _new(rows, ld, torch.int8, device)[:, :n], ld
 
 
 # ------------------------------------------------------------------------------------------------------- norm
 
 def _norm(x, weight, residual, eps, hidden, dense, stream):
-    dtype = _HALF.get(x.dtype) if torch.is_tensor(x) else None
-    if dtype is None:
-        raise ValueError("x must be a float16 or bfloat16 tensor")
-    _matrix("x", x, x.dtype, None)
-    rows, n = x.shape
-    device = x.device
-    _vector("weight", weight, x.dtype, device, n)
+    code, shape, device = _first("x", x, _HALF)
+    dtype = x.dtype
+    ldx = _matrix("x", x, dtype, device, shape)
+    rows, n = shape
+    _vector("weight", weight, dtype, device, n)
+    ldr = ldh = ldy = ldq = 0
     if residual is not None:
-        _matrix("residual", residual, x.dtype, device, x.shape)
+        ldr = _matrix("residual", residual, dtype, device, shape)
+        if hidden is not None:
+            ldh = _matrix("hidden", hidden, dtype, device, shape)
     elif hidden is not None:
         raise ValueError("hidden is an output of the residual's addition: give a residual")
-    if hidden is not None:
-        _matrix("hidden", hidden, x.dtype, device, x.shape)
-    ctx, sp = _on(x, stream)
+    ctx, sp = _on(device, stream)
     with ctx:
         if residual is not None and hidden is None:
-            hidden = torch.empty((rows, n), dtype=x.dtype, device=device)
+            hidden, ldh = _new(rows, n, dtype, device), n
+        y = q = scale = None
         if dense:
-            y, q, scale = torch.empty((rows, n), dtype=x.dtype, device=device), None, None
+            y, ldy = _new(rows, n, dtype, device), n
         else:
-            y, q, scale = None, _codes(rows, n, device), torch.empty(rows, dtype=torch.float32, device=device)
+            q, ldq = _codes(rows, n, device)
+            scale = _empty((rows,), (1,), dtype=torch.float32, device=device)
         _check(LIB.littlebit_rmsnorm_fwd(
-            x.data_ptr(), _ld(x), residual.data_ptr() if residual is not None else None,
-            _ld(residual) if residual is not None else 0, weight.data_ptr(), dtype, rows, n, eps,
-            hidden.data_ptr() if hidden is not None else None, _ld(hidden) if hidden is not None else 0,
-            y.data_ptr() if dense else None, n, q.data_ptr() if q is not None else None,
-            _ld(q) if q is not None else 0, scale.data_ptr() if scale is not None else None, sp))
+            x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(), code, rows, n,
+            eps, None if hidden is None else hidden.data_ptr(), ldh, None if y is None else y.data_ptr(), ldy,
+            None if q is None else q.data_ptr(), ldq, None if scale is None else scale.data_ptr(), sp))
     return y, q, scale, x if residual is None else hidden
 
 
@@ -195,26 +211,22 @@ def littlebit_rmsnorm_bwd(dy: torch.Tensor, hidden: torch.Tensor, weight: torch.
     from the gradients of y and, where it has one, of hidden; dweight in fp32.
     For the 8-bit output, dy is the gradient of the values its codes stand for,
     and the rounding is passed straight through."""
-    dtype = _HALF.get(hidden.dtype) if torch.is_tensor(hidden) else None
-    if dtype is None:
-        raise ValueError("hidden must be a float16 or bfloat16 tensor")
-    _matrix("hidden", hidden, hidden.dtype, None)
-    rows, n = hidden.shape
-    device = hidden.device
-    _matrix("dy", dy, hidden.dtype, device, hidden.shape)
-    _vector("weight", weight, hidden.dtype, device, n)
-    if dhidden is not None:
-        _matrix("dhidden", dhidden, hidden.dtype, device, hidden.shape)
-    ctx, sp = _on(hidden, stream)
+    code, shape, device = _first("hidden", hidden, _HALF)
+    dtype = hidden.dtype
+    ldh = _matrix("hidden", hidden, dtype, device, shape)
+    rows, n = shape
+    lddy = _matrix("dy", dy, dtype, device, shape)
+    _vector("weight", weight, dtype, device, n)
+    lddh = 0 if dhidden is None else _matrix("dhidden", dhidden, dtype, device, shape)
+    ctx, sp = _on(device, stream)
     with ctx:
-        dx = torch.empty((rows, n), dtype=hidden.dtype, device=device)
-        dweight = torch.empty(n, dtype=torch.float32, device=device)
+        dx = _new(rows, n, dtype, device)
+        dweight = _empty((n,), (1,), dtype=torch.float32, device=device)
         need = LIB.littlebit_rmsnorm_bwd_workspace_bytes(rows, n)
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _empty((need,), (1,), dtype=torch.uint8, device=device)
         _check(LIB.littlebit_rmsnorm_bwd(
-            dy.data_ptr(), _ld(dy), dhidden.data_ptr() if dhidden is not None else None,
-            _ld(dhidden) if dhidden is not None else 0, hidden.data_ptr(), _ld(hidden), weight.data_ptr(), dtype,
-            rows, n, eps, dx.data_ptr(), n, dweight.data_ptr(), ws.data_ptr(), need, sp))
+            dy.data_ptr(), lddy, None if dhidden is None else dhidden.data_ptr(), lddh, hidden.data_ptr(), ldh,
+            weight.data_ptr(), code, rows, n, eps, dx.data_ptr(), n, dweight.data_ptr(), ws.data_ptr(), need, sp))
     return dx, dweight
 
 
@@ -222,17 +234,14 @@ def littlebit_rmsnorm_bwd(dy: torch.Tensor, hidden: torch.Tensor, weight: torch.
 
 def littlebit_q8_quantize(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(q, scale): int8 codes of each row with one fp32 scale, largest value 127."""
-    dtype = _DTYPE.get(x.dtype) if torch.is_tensor(x) else None
-    if dtype is None:
-        raise ValueError("x must be a float32, float16 or bfloat16 tensor")
-    _matrix("x", x, x.dtype, None)
-    rows, n = x.shape
-    ctx, sp = _on(x, stream)
+    code, shape, device = _first("x", x, _DTYPE)
+    ldx = _matrix("x", x, x.dtype, device, shape)
+    rows, n = shape
+    ctx, sp = _on(device, stream)
     with ctx:
-        q = _codes(rows, n, x.device)
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-        _check(LIB.littlebit_q8_quantize(x.data_ptr(), _ld(x), dtype, rows, n, q.data_ptr(), _ld(q),
-                                         scale.data_ptr(), sp))
+        q, ldq = _codes(rows, n, device)
+        scale = _empty((rows,), (1,), dtype=torch.float32, device=device)
+        _check(LIB.littlebit_q8_quantize(x.data_ptr(), ldx, code, rows, n, q.data_ptr(), ldq, scale.data_ptr(), sp))
     return q, scale
 
 
@@ -241,26 +250,24 @@ def littlebit_q8_linear_fwd(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Te
                             stream=None) -> torch.Tensor:
     """y[t, o] = xscale[t] * wscale[o] * sum_k xq[t, k] * wq[o, k] in `dtype`
     (that of `out`, where it is given)."""
-    _matrix("xq", xq, torch.int8, None)
-    device = xq.device
-    _matrix("wq", wq, torch.int8, device)
-    batch, n = xq.shape
-    m = wq.shape[0]
-    if wq.shape[1] != n:
-        raise ValueError(f"wq has rows of {wq.shape[1]}, xq of {n}")
+    _, (batch, n), device = _first("xq", xq, _INT8)
+    ldx = _matrix("xq", xq, torch.int8, device, (batch, n))
+    m = _first("wq", wq, _INT8)[1][0]
+    ldw = _matrix("wq", wq, torch.int8, device, (m, n))
     _vector("xscale", xscale, torch.float32, device, batch)
     _vector("wscale", wscale, torch.float32, device, m)
+    ldy = m
     if out is not None:
         dtype = out.dtype
-        _matrix("out", out, dtype, device, (batch, m))
+        ldy = _matrix("out", out, dtype, device, (batch, m))
     code = _DTYPE.get(dtype)
     if code is None:
         raise ValueError("the output must be float32, float16 or bfloat16")
-    ctx, sp = _on(xq, stream)
+    ctx, sp = _on(device, stream)
     with ctx:
-        y = out if out is not None else torch.empty((batch, m), dtype=dtype, device=device)
-        _check(LIB.littlebit_q8_linear_fwd(xq.data_ptr(), _ld(xq), xscale.data_ptr(), wq.data_ptr(), _ld(wq),
-                                           wscale.data_ptr(), batch, m, n, y.data_ptr(), _ld(y), code, sp))
+        y = out if out is not None else _new(batch, m, dtype, device)
+        _check(LIB.littlebit_q8_linear_fwd(xq.data_ptr(), ldx, xscale.data_ptr(), wq.data_ptr(), ldw,
+                                           wscale.data_ptr(), batch, m, n, y.data_ptr(), ldy, code, sp))
     return y
 
 
@@ -273,30 +280,30 @@ def littlebit_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
     negative target stands for no token (logprob 0).  lse holds each row's
     maximum and, behind it, log sum exp(x - maximum): lse.sum(0) is the
     logarithm of the sum of exponentials."""
-    code = _DTYPE.get(logits.dtype) if torch.is_tensor(logits) else None
-    if code is None:
-        raise ValueError("logits must be a float32, float16 or bfloat16 tensor")
-    _matrix("logits", logits, logits.dtype, None)
-    rows, vocab = logits.shape
-    device = logits.device
+    code, shape, device = _first("logits", logits, _DTYPE)
+    ld = _matrix("logits", logits, logits.dtype, device, shape)
+    rows, vocab = shape
     if targets is not None:
         _vector("targets", targets, torch.int64, device, rows)
-    ctx, sp = _on(logits, stream)
+    ctx, sp = _on(device, stream)
     with ctx:
-        stats = torch.empty((4, rows), dtype=torch.float32, device=device)
-        logprob, entropy, lse = stats[0], stats[1], stats[2:]
-        values = places = None
+        logprob = values = places = ws = None
+        if targets is not None:
+            logprob = _empty((rows,), (1,), dtype=torch.float32, device=device)
+        entropy = _empty((rows,), (1,), dtype=torch.float32, device=device)
+        lse = _new(2, rows, torch.float32, device)
         if top > 0:
-            values = torch.empty((rows, top), dtype=torch.float32, device=device)
-            places = torch.empty((rows, top), dtype=torch.int64, device=device)
+            values = _new(rows, top, torch.float32, device)
+            places = _new(rows, top, torch.int64, device)
         need = LIB.littlebit_logprobs_workspace_bytes(rows, vocab, code, top)
-        ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        if need:
+            ws = _empty((need,), (1,), dtype=torch.uint8, device=device)
         _check(LIB.littlebit_logprobs_fwd(
-            logits.data_ptr(), _ld(logits), code, rows, vocab, targets.data_ptr() if targets is not None else None,
-            logprob.data_ptr() if targets is not None else None, entropy.data_ptr(), lse.data_ptr(), top,
-            values.data_ptr() if values is not None else None, places.data_ptr() if places is not None else None,
-            ws.data_ptr() if ws is not None else None, need, sp))
-    return logprob if targets is not None else None, entropy, lse, values, places
+            logits.data_ptr(), ld, code, rows, vocab, None if targets is None else targets.data_ptr(),
+            None if logprob is None else logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top,
+            None if values is None else values.data_ptr(), None if places is None else places.data_ptr(),
+            None if ws is None else ws.data_ptr(), need, sp))
+    return logprob, entropy, lse, values, places
 
 
 def littlebit_logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor], lse: torch.Tensor,
@@ -308,12 +315,9 @@ def littlebit_logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
     littlebit_logprobs_fwd's logprob, entropy and top_logprob (None: it has
     none).  lse, entropy and top_index are that call's outputs.  ``out`` may be
     the logits themselves."""
-    code = _DTYPE.get(logits.dtype) if torch.is_tensor(logits) else None
-    if code is None:
-        raise ValueError("logits must be a float32, float16 or bfloat16 tensor")
-    _matrix("logits", logits, logits.dtype, None)
-    rows, vocab = logits.shape
-    device = logits.device
+    code, shape, device = _first("logits", logits, _DTYPE)
+    ld = _matrix("logits", logits, logits.dtype, device, shape)
+    rows, vocab = shape
     _table("lse", lse, torch.float32, device, (2, rows))
     if dlogprob is not None:
         if targets is None:
@@ -332,18 +336,15 @@ def littlebit_logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
         top = dtop.shape[1]
         _table("top_index", top_index, torch.int64, device, (rows, top))
         _table("dtop", dtop, torch.float32, device, (rows, top))
-    if out is not None:
-        _matrix("out", out, logits.dtype, device, logits.shape)
-    ctx, sp = _on(logits, stream)
+    ldd = vocab if out is None else _matrix("out", out, logits.dtype, device, shape)
+    ctx, sp = _on(device, stream)
     with ctx:
-        d = out if out is not None else torch.empty((rows, vocab), dtype=logits.dtype, device=device)
+        d = _new(rows, vocab, logits.dtype, device) if out is None else out
         _check(LIB.littlebit_logprobs_bwd(
-            logits.data_ptr(), _ld(logits), code, rows, vocab,
-            targets.data_ptr() if dlogprob is not None else None, lse.data_ptr(),
-            entropy.data_ptr() if dentropy is not None else None,
-            dlogprob.data_ptr() if dlogprob is not None else None,
-            dentropy.data_ptr() if dentropy is not None else None, top,
-            top_index.data_ptr() if top else None, dtop.data_ptr() if top else None, d.data_ptr(), _ld(d), sp))
+            logits.data_ptr(), ld, code, rows, vocab, None if dlogprob is None else targets.data_ptr(), lse.data_ptr(),
+            None if dentropy is None else entropy.data_ptr(), None if dlogprob is None else dlogprob.data_ptr(),
+            None if dentropy is None else dentropy.data_ptr(), top, top_index.data_ptr() if top else None,
+            dtop.data_ptr() if top else None, d.data_ptr(), ldd, sp))
     return d
 
 
