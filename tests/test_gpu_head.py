@@ -210,7 +210,8 @@ def test_quantize_ends_of_the_range(head):
 
 LINEAR = [(1, 1, 1), (1, 16, 64), (2, 17, 65), (3, 100, 128), (16, 33, 1000), (17, 64, 256), (31, 130, 320), (64, 48, 2048),
           (65, 129, 512), (100, 200, 511), (128, 256, 1024), (130, 300, 640), (257, 513, 192), (300, 1000, 4096),
-          (520, 768, 128), (1, 4096, 13824), (5, 32000, 320)]
+          (520, 768, 128), (1, 4096, 13824), (5, 32000, 320), (16, 4500, 272), (7, 9001, 144), (3, 8200, 130), (1, 4112, 16),
+          (16, 4200, 9600), (2, 33000, 48), (12, 4128, 4096), (40, 1100, 200), (90, 4300, 390), (260, 9000, 256), (600, 9000, 384)]
 
 
 @pytest.mark.parametrize("batch,m,n", LINEAR)
