@@ -188,87 +188,141 @@ void launch_norm(const LbNormArgs& a, hipStream_t stream) {
 // -------------------------------------------------------------------- backward
 // With u = w dy:  dx = dhidden + r u - h (r^3 / n) sum(u h);  both sums
 // (h^2 for r, and u h) run over the row in one exchange, so r need not be kept
-// from the forward pass.  dweight = sum over rows of dy h r: a group keeps its
-// rows' sum in registers and writes it once; a second kernel adds the groups
-// in a fixed order.
-template <typename T, int G, int V>
-__global__ __launch_bounds__(G) void lb_norm_bwd_kernel(const LbNormBwdArgs A) {
-  __shared__ float part[2][2][G / 64];
-  const int t = threadIdx.x, w = wave_id(), lane = t & 63;
-  float wt[V][8], dw[V][8];
+// from the forward pass.  dweight = sum over rows of dy h r: a thread keeps the
+// sum of its columns over its rows in registers, the R rows that a workgroup
+// holds at a time join theirs in LDS at the end, and a second kernel adds the
+// workgroups, all in a fixed order.  The next row's loads are under way while a
+// row is reduced.
+template <typename T, int V>
+struct RowIn {
+  u32x4 h[V], dy[V], dh[V];
+};
+// Eight 2-byte elements as they lie in memory, zeros behind the row.
+template <typename T>
+__device__ __forceinline__ u32x4 raw8(const T* p, long left) {
+  if (left >= 8) return load_any<u32x4>(p);
+  T e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = i < left ? p[i] : (T)0.0f;
+  u32x4 w;
+  __builtin_memcpy(&w, e, sizeof w);
+  return w;
+}
+template <typename T>
+__device__ __forceinline__ float part_of(const u32x4& w, int e) {
+  return e & 1 ? Pair<T>::hi(w[e >> 1]) : Pair<T>::lo(w[e >> 1]);
+}
+
+template <typename T, int G, int R, int V>
+__global__ __launch_bounds__(G * R) void lb_norm_bwd_kernel(const LbNormBwdArgs A) {
+  constexpr int kW = G / 64;
+  constexpr bool kAhead = V == 1;  // registers for the next row
+  constexpr bool kInLds = V == 4;  // the columns' sums (128 KB) in LDS: no registers for them
+  __shared__ float part[2][2][R][kW];
+  __shared__ float join[kInLds ? G * V * 8 : R > 1 ? (R - 1) * G * V * 8 : 1];
+  const int t = threadIdx.x % G, rg = threadIdx.x / G, w = wave_id() % kW, lane = threadIdx.x & 63;
+  u32x4 wt[V];
+  float dw[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int k = 8 * (t + i * G);
-    if (k < A.n) {
-      load8((const T*)A.weight + k, (long)A.n - k, 0.0f, wt[i]);
-    } else {
+    wt[i] = raw8((const T*)A.weight + k, (long)A.n - k);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wt[i][e] = 0.0f;
+    for (int e = 0; e < 8; ++e) {
+      dw[i][e] = 0.0f;
+      if constexpr (kInLds) join[(i * 8 + e) * G + t] = 0.0f;  // this thread's alone
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
   }
-  int flip = 0;
-  for (long row = blockIdx.x; row < A.rows; row += gridDim.x, flip ^= 1) {
-    float h[V][8], dy[V][8], dh[V][8];
-    float s2 = 0.0f, uh = 0.0f;
+  const long stride = (long)gridDim.x * R;
+  const long rounds = (A.rows + stride - 1) / stride;
+  auto load = [&](long row, RowIn<T, V>& in) __attribute__((always_inline)) {
+    const bool real = row < A.rows;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int k = 8 * (t + i * G);
-      const long left = A.n - k;
-      if (left > 0) {
-        load8((const T*)A.hidden + row * A.ldh + k, left, 0.0f, h[i]);
-        load8((const T*)A.dy + row * A.lddy + k, left, 0.0f, dy[i]);
-        if (A.dhidden) load8((const T*)A.dhidden + row * A.lddh + k, left, 0.0f, dh[i]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = dy[i][e] = 0.0f;
-      }
-      if (!A.dhidden || left <= 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dh[i][e] = 0.0f;
-      }
+      const long left = real ? (long)A.n - k : 0;
+      in.h[i] = raw8((const T*)A.hidden + row * A.ldh + k, left);
+      in.dy[i] = raw8((const T*)A.dy + row * A.lddy + k, left);
+      in.dh[i] = raw8((const T*)A.dhidden + row * A.lddh + k, A.dhidden ? left : 0);
     }
+  };
+  RowIn<T, V> next;
+  long row = (long)blockIdx.x * R + rg;
+  load(row, next);
+  for (long j = 0; j < rounds; ++j, row += stride) {
+    if (!kAhead && j > 0) load(row, next);
+    const RowIn<T, V> in = next;
+    if (kAhead && j + 1 < rounds) load(row + stride, next);
+    float s2 = 0.0f, uh = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s2 += h[i][e] * h[i][e];
-        uh += wt[i][e] * dy[i][e] * h[i][e];
+        const float h = part_of<T>(in.h[i], e);
+        s2 += h * h;
+        uh += part_of<T>(wt[i], e) * part_of<T>(in.dy[i], e) * h;
       }
     }
     s2 = wave_sum(s2);
     uh = wave_sum(uh);
-    if (lane == 0) {
-      part[flip][0][w] = s2;
-      part[flip][1][w] = uh;
-    }
-    __syncthreads();  // two buffers in turn: one barrier a row is enough
-    s2 = part[flip][0][0];
-    uh = part[flip][1][0];
+    if constexpr (kW > 1) {
+      const int flip = j & 1;
+      if (lane == 0) {
+        part[flip][0][rg][w] = s2;
+        part[flip][1][rg][w] = uh;
+      }
+      __syncthreads();  // two buffers in turn: one barrier a row is enough
+      s2 = part[flip][0][rg][0];
+      uh = part[flip][1][rg][0];
 #pragma unroll
-    for (int i = 1; i < G / 64; ++i) {
-      s2 += part[flip][0][i];
-      uh += part[flip][1][i];
+      for (int i = 1; i < kW; ++i) {
+        s2 += part[flip][0][rg][i];
+        uh += part[flip][1][rg][i];
+      }
     }
     const float r = 1.0f / sqrtf(s2 / (float)A.n + A.eps);
     const float c = (uh * r) * r / (float)A.n;
+    const bool real = row < A.rows;  // behind the last row there are zeros; with eps = 0 their r is infinite
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int k = 8 * (t + i * G);
       float d[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float hr = h[i][e] * r;
-        d[e] = dh[i][e] + (r * (wt[i][e] * dy[i][e]) - hr * c);
-        dw[i][e] += dy[i][e] * hr;
+        const float hr = part_of<T>(in.h[i], e) * r, dy = part_of<T>(in.dy[i], e);
+        d[e] = part_of<T>(in.dh[i], e) + (r * (part_of<T>(wt[i], e) * dy) - hr * c);
+        if constexpr (kInLds) {
+          if (real) join[(i * 8 + e) * G + t] += dy * hr;
+        } else {
+          if (real) dw[i][e] += dy * hr;
+        }
       }
-      store8((T*)A.dx + row * A.lddx + k, (long)A.n - k, d);
+      store8((T*)A.dx + row * A.lddx + k, real ? (long)A.n - k : 0, d);
     }
+  }
+  if constexpr (R > 1) {
+    if (rg > 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) join[((rg - 1) * V * 8 + i * 8 + e) * G + t] = dw[i][e];
+    }
+    __syncthreads();
+    if (rg > 0) return;
+#pragma unroll
+    for (int q = 0; q < R - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] += join[(q * V * 8 + i * 8 + e) * G + t];
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int k = 8 * (t + i * G);
+    if constexpr (kInLds) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[i][e] = join[(i * 8 + e) * G + t];
+    }
     store8(A.partial + (long)blockIdx.x * A.n + k, (long)A.n - k, dw[i]);
   }
 }
@@ -281,8 +335,17 @@ __global__ __launch_bounds__(1024) void lb_norm_dweight_kernel(const float* __re
   const int c = threadIdx.x & 31, p = threadIdx.x >> 5;
   const int k = blockIdx.x * 32 + c;
   float v = 0.0f;
-  if (k < n)
-    for (int g = p; g < groups; g += 32) v += partial[(long)g * n + k];
+  if (k < n) {
+    int g = p;
+    for (; g + 32 * 7 < groups; g += 32 * 8) {
+      float q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = partial[(long)(g + 32 * i) * n + k];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += q[i];
+    }
+    for (; g < groups; g += 32) v += partial[(long)g * n + k];
+  }
   s[p][c] = v;
   __syncthreads();
   if (p == 0 && k < n) {
@@ -292,23 +355,38 @@ __global__ __launch_bounds__(1024) void lb_norm_dweight_kernel(const float* __re
   }
 }
 
-template <typename T, int G, int V>
+// Threads a row and rows a workgroup holds at a time.
+struct BwdShape {
+  int g, r, v;
+};
+BwdShape bwd_shape(int64_t n) {
+  if (n <= 512) return {64, 16, 1};
+  if (n <= 2048) return {256, 4, 1};
+  if (n <= 4096) return {512, 2, 1};
+  if (n <= 8192) return {1024, 1, 1};
+  return {1024, 1, n <= 16384 ? 2 : 4};
+}
+
+template <typename T, int G, int R, int V>
 void launch_bwd_one(const LbNormBwdArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((lb_norm_bwd_kernel<T, G, V>), dim3((unsigned)a.groups), dim3(G), 0, stream, a);
+  hipLaunchKernelGGL((lb_norm_bwd_kernel<T, G, R, V>), dim3((unsigned)a.groups), dim3(G * R), 0, stream, a);
 }
 
 template <typename T>
 void launch_bwd(const LbNormBwdArgs& a, hipStream_t stream) {
-  if (a.n <= 2048)
-    launch_bwd_one<T, 256, 1>(a, stream);
-  else if (a.n <= 4096)
-    launch_bwd_one<T, 512, 1>(a, stream);
-  else if (a.n <= 8192)
-    launch_bwd_one<T, 1024, 1>(a, stream);
-  else if (a.n <= 16384)
-    launch_bwd_one<T, 1024, 2>(a, stream);
+  const BwdShape s = bwd_shape(a.n);
+  if (s.g == 64)
+    launch_bwd_one<T, 64, 16, 1>(a, stream);
+  else if (s.g == 256)
+    launch_bwd_one<T, 256, 4, 1>(a, stream);
+  else if (s.g == 512)
+    launch_bwd_one<T, 512, 2, 1>(a, stream);
+  else if (s.v == 1)
+    launch_bwd_one<T, 1024, 1, 1>(a, stream);
+  else if (s.v == 2)
+    launch_bwd_one<T, 1024, 1, 2>(a, stream);
   else
-    launch_bwd_one<T, 1024, 4>(a, stream);
+    launch_bwd_one<T, 1024, 1, 4>(a, stream);
 }
 
 }  // namespace
@@ -331,9 +409,10 @@ hipError_t lb_launch_q8_quantize(const LbNormArgs& a, int dtype, hipStream_t str
   return hipGetLastError();
 }
 
+// Workgroups of the backward pass: one a compute unit, fewer for few rows.
 int lb_norm_bwd_groups(int64_t rows, int64_t n) {
-  (void)n;
-  return (int)(rows < 512 ? rows : 512);
+  const int64_t r = bwd_shape(n).r, groups = (rows + r - 1) / r;
+  return (int)(groups < 256 ? groups : 256);
 }
 
 hipError_t lb_launch_norm_bwd(const LbNormBwdArgs& a, int dtype, hipStream_t stream) {
