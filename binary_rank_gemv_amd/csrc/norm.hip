@@ -169,16 +169,23 @@ void launch_one(const LbNormArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((lb_norm_kernel<T, G, V, QUANT>), dim3((unsigned)blocks), dim3(G < 256 ? 256 : G), 0, stream, a);
 }
 
+// Threads a row by its length, and more of them, with fewer vectors each, while
+// there are few rows: one row of 5120 takes 5.3 us with 256 threads, 3.8 with 512,
+// 3.4 with 1024; 4096 rows take 38.8, 34.7 and 40.0.
 template <typename T, bool QUANT>
 void launch_norm(const LbNormArgs& a, hipStream_t stream) {
   if (a.n <= 512)
     launch_one<T, 64, 1, QUANT>(a, stream);
   else if (a.n <= 2048)
     launch_one<T, 256, 1, QUANT>(a, stream);
-  else if (a.n <= 4096)
+  else if (a.n <= 4096 && a.rows > 512)
     launch_one<T, 256, 2, QUANT>(a, stream);
+  else if (a.n <= 4096)
+    launch_one<T, 512, 1, QUANT>(a, stream);
+  else if (a.n <= 8192 && a.rows > 256)
+    launch_one<T, 512, 2, QUANT>(a, stream);
   else if (a.n <= 8192)
-    launch_one<T, 256, 4, QUANT>(a, stream);
+    launch_one<T, 1024, 1, QUANT>(a, stream);
   else if (a.n <= 16384)
     launch_one<T, 1024, 2, QUANT>(a, stream);
   else

@@ -59,7 +59,7 @@ def case(*what):
 # ----------------------------------------------------------------------------------------------------------- norm
 
 NORM_SHAPES = [(1, 1), (1, 7), (3, 8), (5, 100), (4, 512), (2, 513), (3, 2048), (2, 2056), (1, 4096), (1, 5120), (3, 8192),
-               (2, 8200), (1, 16384), (2, 16385), (1, 32768)]
+               (2, 8200), (1, 16384), (2, 16385), (1, 32768), (530, 2500), (270, 5000)]
 
 
 def chain(n):
