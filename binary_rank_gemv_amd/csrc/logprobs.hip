@@ -244,6 +244,8 @@ __device__ __forceinline__ u64 block_top(const u64* keys, int count, u64 (*room)
   return list;
 }
 
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));  // at any byte
+
 template <typename T>
 struct Chunk {
   u32x4 w[kEpt * sizeof(T) / 16];
@@ -265,6 +267,16 @@ __device__ __forceinline__ void chunk_load(Chunk<T>& C, const T* x, long c, long
       __builtin_memcpy(&C.w[h * kW], e, sizeof e);
     }
   }
+}
+template <typename T>
+__device__ __forceinline__ void chunk_load_whole(Chunk<T>& C, const T* x, int t) {
+  constexpr int kW = sizeof(T) / 2;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < kW; ++j)
+      C.w[h * kW + j] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4_any*>((const char*)(x + 8 * (t + h * kThreads)) + 16 * j));
 }
 template <typename T>
 __device__ __forceinline__ void chunk_values(const Chunk<T>& C, float (&v)[kEpt]) {
@@ -298,12 +310,9 @@ __global__ __launch_bounds__(kThreads) void lb_logprobs_kernel(const LbLogprobsA
   float largest = -INFINITY;
   const int per = (int)((end - begin + kKept * kChunk - 1) / (kKept * kChunk));  // chunks a kept maximum
   int slot = 0, in_slot = 0;
-  Chunk<T> next;
-  chunk_load<T>(next, x, begin, end, t);
-  for (long c = begin; c < end; c += kChunk) {
+  auto take = [&](const Chunk<T>& chunk) __attribute__((always_inline)) {
     float v[kEpt];
-    chunk_values(next, v);
-    if (c + kChunk < end) chunk_load<T>(next, x, c + kChunk, end, t);
+    chunk_values(chunk, v);
     float most = v[0];
 #pragma unroll
     for (int i = 1; i < kEpt; ++i) most = max_nan(most, v[i]);
@@ -328,6 +337,23 @@ __global__ __launch_bounds__(kThreads) void lb_logprobs_kernel(const LbLogprobsA
         ++slot;
       }
     }
+  };
+  // whole chunks, the next one's loads (of the last: itself again) under way while
+  // one is taken; then what is left
+  const int whole = (int)((end - begin) / kChunk);
+  Chunk<T> chunk, next;
+  const T* at = x + begin;
+  if (whole > 0) chunk_load_whole<T>(chunk, at, t);
+  for (int j = 0; j < whole; ++j) {
+    if (j + 1 < whole) at += kChunk;
+    chunk_load_whole<T>(next, at, t);
+    __builtin_amdgcn_sched_barrier(0);
+    take(chunk);
+    chunk = next;
+  }
+  if (begin + (long)whole * kChunk < end) {
+    chunk_load<T>(chunk, x, begin + (long)whole * kChunk, end, t);
+    take(chunk);
   }
   S = wave_join(S);
   if (lane == 0) stat[w] = S;
