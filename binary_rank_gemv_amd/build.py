@@ -110,6 +110,26 @@ def build_sanitized_host(verbose: bool = False) -> str:
     return SANITIZED_LIB
 
 
+SANITIZED_HEAD_LIB = os.path.join(LIBDIR, "sanitized", "liblittlebit_head.so")
+
+
+def build_sanitized_head(verbose: bool = False) -> str:
+    """The same for the dense operators' library (head_host.hip); load it with
+    LITTLEBIT_HEAD_LIBRARY=<path>."""
+    objdir = os.path.join(LIBDIR, "sanitized")
+    os.makedirs(objdir, exist_ok=True)
+    host = os.path.join(objdir, "head_host.hip.o")
+    _run([HIPCC, "--offload-arch=gfx950", "-O1", "-g", "-std=c++17", "-fPIC", "-c",
+          "-I", os.path.join(ROOT, "include"), "-I", CSRC, *DEVICE_FLAGS, *SANITIZE_HOST_FLAGS,
+          "-Xarch_host", "-fno-omit-frame-pointer", os.path.join(CSRC, "head_host.hip"), "-o", host], verbose)
+    others = [os.path.join(OBJDIR, f + ".o") for f in HEAD_SOURCES if f != "head_host.hip"]
+    missing = [o for o in others if not os.path.exists(o)]
+    if missing:
+        raise RuntimeError(f"build the library first; missing {missing}")
+    _link([host, *others], SANITIZED_HEAD_LIB, [*SANITIZE_HOST_FLAGS, "-shared-libsan"], verbose)
+    return SANITIZED_HEAD_LIB
+
+
 STAMPED_LIB = os.path.join(LIBDIR, "stamped", "liblittlebit.so")
 
 

@@ -179,6 +179,8 @@ lb_status littlebit_q8_linear_fwd(const int8_t* xq, int64_t ldx, const float* xs
   LB_TRY(check_rows(name, batch, n, kMaxCodes));
   if (m < 1) return fail(LB_ERR_INVALID_ARG, "%s: m=%lld must be >= 1", name, (long long)m);
   if (m > (1 << 24)) return fail(LB_ERR_UNSUPPORTED, "%s: m=%lld exceeds %d", name, (long long)m, 1 << 24);
+  if (batch * m > (1ll << 38))
+    return fail(LB_ERR_UNSUPPORTED, "%s: %lld x %lld outputs are too many for one call", name, (long long)batch, (long long)m);
   if (batch == 0) return LB_OK;
   LB_TRY(check_matrix(name, "xq", xq, ldx, n, 1));
   LB_TRY(check_matrix(name, "wq", wq, ldw, n, 1));

@@ -104,7 +104,8 @@ lb_status littlebit_q8_quantize(const void *x, int64_t ldx, int dtype, int64_t r
  *   xq        batch rows of n codes; wq m rows of n codes.
  *   xscale    fp32 [batch]; wscale fp32 [m].
  *   y         batch rows of m values, y_dtype LB_F32, LB_F16 or LB_BF16.
- * batch >= 0, m >= 1, 1 <= n <= 131071 (where 128^2 n stays below 2^31).
+ * batch >= 0, m >= 1, 1 <= n <= 131071 (where 128^2 n stays below 2^31),
+ * batch x m <= 2^38.
  */
 lb_status littlebit_q8_linear_fwd(const int8_t *xq, int64_t ldx, const float *xscale,
                                   const int8_t *wq, int64_t ldw, const float *wscale, int64_t batch,

@@ -452,6 +452,93 @@ def test_logprobs_backward_of_rows_masked_with_the_lowest_value(head, dt):
     assert abs(lp[0].item() + np.log(1000)) <= 8 * U * 7 and abs(H[0].item() - np.log(1000)) <= 40 * U * 7
 
 
+def test_logprobs_backward_of_a_place_given_twice(head):
+    """The target among the alternatives, and one alternative given twice: every gradient counts."""
+    case("logprobs backward, places twice")
+    x = randn(3, 2, 50)
+    targets = torch.tensor([7, 7])
+    lp, H, lse, _, _ = head.littlebit_logprobs_fwd(x.float().cuda(), targets.cuda())
+    idx = torch.tensor([[7, 9, 9], [0, 49, 0]])
+    g, gt = torch.tensor([0.5, -1.0]), torch.tensor([[1.0, 2.0, 3.0], [0.25, 0.5, 0.75]])
+    d = head.littlebit_logprobs_bwd(x.float().cuda(), targets.cuda(), lse, None, g.cuda(), None, idx.cuda(), gt.cuda())
+    want = oh.logprobs_backward(f64(x.float()), targets.numpy(), g.numpy(), None, idx.numpy(), gt.numpy())
+    assert np.abs(f64(d) - want).max() <= 100 * U * 8
+
+
+def test_logprobs_backward_leaves_what_lies_between_rows(head):
+    case("logprobs backward, surroundings")
+    buf = torch.full((5 * 140 + 20,), 3.0, dtype=torch.float16, device="cuda")
+    out = buf[10:10 + 5 * 140].view(5, 140)[:, :133]
+    x = randn(8, 5, 133).half().cuda()
+    targets = torch.arange(5, device="cuda")
+    lp, H, lse, _, _ = head.littlebit_logprobs_fwd(x, targets)
+    one = torch.ones(5, device="cuda")
+    got = head.littlebit_logprobs_bwd(x, targets, lse, H, one, one, out=out)
+    assert got.data_ptr() == out.data_ptr()
+    assert torch.equal(out, head.littlebit_logprobs_bwd(x, targets, lse, H, one, one))
+    outside = torch.ones_like(buf, dtype=torch.bool)
+    outside[10:10 + 5 * 140].view(5, 140)[:, :133] = False
+    assert (buf[outside] == 3).all()
+
+
+def test_rows_beyond_32_bits(head):
+    """Rows whose offsets pass 2^31 (and 2^32 bytes): the same as the same rows close together."""
+    case("rows far apart")
+    far = torch.empty(5_000_000_000, dtype=torch.int8, device="cuda")   # 5 GB, read and written at the rows alone
+
+    def spread(t, ld):
+        v = torch.as_strided(far.view(t.dtype), t.shape, (ld, 1), 8)
+        v.copy_(t)
+        return v
+
+    x, w = randn(1, 24, 640).half().cuda(), torch.ones(640, dtype=torch.float16, device="cuda")
+    y, _ = head.littlebit_rmsnorm_fwd(spread(x, 100_000_000), w)
+    assert torch.equal(y, head.littlebit_rmsnorm_fwd(x, w)[0])
+    dx, dw = head.littlebit_rmsnorm_bwd(spread(x, 100_000_000), x, w)
+    assert all(torch.equal(a, b) for a, b in zip((dx, dw), head.littlebit_rmsnorm_bwd(x, x, w)))
+    q, s = head.littlebit_q8_quantize(spread(x, 100_000_000))
+    assert torch.equal(q, head.littlebit_q8_quantize(x)[0])
+    q = q.contiguous()
+    for m in (24, 4800):       # channels as rows far apart; tokens as rows far apart
+        W = torch.randint(-127, 128, (m, 640), dtype=torch.int8, device="cuda")
+        ws = torch.rand(m, device="cuda")
+        for batch in (3, 24):
+            want = head.littlebit_q8_linear_fwd(q[:batch], s[:batch], W, ws)
+            if m == 24:
+                far_w = head.littlebit_q8_linear_fwd(q[:batch], s[:batch], spread(W, 200_000_000), ws)
+                assert torch.equal(far_w, want)
+            far_x = head.littlebit_q8_linear_fwd(spread(q[:batch], 200_000_000), s[:batch], W, ws)
+            assert torch.equal(far_x, want)
+            out = torch.as_strided(far.view(torch.float16), (batch, m), (100_000_000, 1), 8)
+            assert torch.equal(head.littlebit_q8_linear_fwd(q[:batch], s[:batch], W, ws, out=out), want)
+    lg, tg = randn(2, 24, 5000).half().cuda(), torch.arange(24, device="cuda")
+    a = head.littlebit_logprobs_fwd(spread(lg, 100_000_000), tg, 3)
+    b = head.littlebit_logprobs_fwd(lg, tg, 3)
+    assert all(torch.equal(p, r) for p, r in zip(a, b))
+    one = torch.ones(24, device="cuda")
+    v = spread(lg, 100_000_000)
+    d = head.littlebit_logprobs_bwd(v, tg, b[2], b[1], one, one, out=v)
+    assert torch.equal(d, head.littlebit_logprobs_bwd(lg, tg, b[2], b[1], one, one))
+
+
+def test_many_rows(head):
+    """More logits than 2^31 in one call: the last rows are the rows themselves."""
+    case("many rows")
+    rows, vocab = 70_000, 32_000
+    x = torch.empty(rows, vocab, dtype=torch.float16, device="cuda").normal_()
+    targets = torch.randint(0, vocab, (rows,), device="cuda")
+    a = head.littlebit_logprobs_fwd(x, targets, 2)
+    for r in (0, 67_108, 67_109, 69_999):
+        b = head.littlebit_logprobs_fwd(x[r:r + 1].clone(), targets[r:r + 1], 2)
+        assert torch.equal(a[0][r:r + 1], b[0]) and torch.equal(a[1][r:r + 1], b[1])
+        assert torch.equal(a[3][r:r + 1], b[3]) and torch.equal(a[4][r:r + 1], b[4])
+    last = x[-1:].clone()
+    one = torch.ones(rows, device="cuda")
+    head.littlebit_logprobs_bwd(x, targets, a[2], a[1], one, one, out=x)
+    b = head.littlebit_logprobs_fwd(last, targets[-1:])
+    assert torch.equal(x[-1:], head.littlebit_logprobs_bwd(last, targets[-1:], b[2], b[1], one[:1], one[:1]))
+
+
 # ------------------------------------------------------------------------------------------------------- together
 
 def _model(head, n=512, vocab=2000, seed=3):

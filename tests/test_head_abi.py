@@ -95,6 +95,7 @@ def _lin(xq=FAKE, ldx=64, xs=FAKE, wq=FAKE, ldw=64, ws=FAKE, batch=2, m=16, n=64
     (dict(ldx=63), BAD), (dict(ldw=63), BAD), (dict(ldy=15), BAD), (dict(batch=-1), BAD), (dict(m=0), BAD),
     (dict(n=0), BAD), (dict(n=131072, ldx=131072, ldw=131072), UNSUP), (dict(m=1 << 25, ldy=1 << 25), UNSUP),
     (dict(dt=9), BAD), (dict(y=FAKE + 1), BAD), (dict(xs=FAKE + 1), BAD),
+    (dict(batch=1 << 20, m=1 << 20, ldy=1 << 20), UNSUP),
 ])
 def test_linear_refuses(kw, status):
     assert _lin(**kw) == status
