@@ -568,8 +568,11 @@ void launch_few(const LbQ8LinearArgs& a, int ncu, hipStream_t stream) {
 
 // The tile shape whose rounds of workgroups over the compute units take the
 // least, counted in hundredths of a us a chunk as measured with one workgroup
-// a compute unit.  Against all shapes on fifteen sizes (24 to 2000 tokens, 4096 to
-// 32000 channels) this choice was the fastest or within 4%, once within 18%.
+// a compute unit.  Against all shapes on fourteen sizes (24 to 2000 tokens, 4096 to
+// 32000 channels) this choice was the fastest or within 4%: 64 x 5120 -> 32000 in
+// 128 x 64 35 us (64 x 64 41, 128 x 128 38), 300 x 5120 -> 5120 in 64 x 128 18 (22, 26),
+// 201 x 5120 -> 13824 in 128 x 128 31 (64 x 128 38, 128 x 256 44), 512 x 4096 -> 11008 in
+// 128 x 256 33 (128 x 128 44, 256 x 256 57).
 template <typename Y>
 void launch_linear(const LbQ8LinearArgs& a, hipStream_t stream) {
   const int ncu = cu_count();
@@ -579,10 +582,10 @@ void launch_linear(const LbQ8LinearArgs& a, hipStream_t stream) {
   }
   static const struct {
     int bm, bn, cost;
-  } shapes[] = {{32, 64, 11}, {64, 64, 14}, {128, 64, 24}, {128, 128, 39}, {128, 256, 68}, {256, 256, 133}};
+  } shapes[] = {{32, 64, 11}, {64, 64, 14}, {64, 128, 23}, {128, 64, 24}, {128, 128, 39}, {128, 256, 68}, {256, 256, 133}};
   int best = 0;
   long least = 0;
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < 7; ++i) {
     const long wgs = (long)((a.m + shapes[i].bm - 1) / shapes[i].bm) * ((a.batch + shapes[i].bn - 1) / shapes[i].bn);
     const long cost = (wgs + ncu - 1) / ncu * shapes[i].cost;
     if (i == 0 || cost < least) {
@@ -593,9 +596,10 @@ void launch_linear(const LbQ8LinearArgs& a, hipStream_t stream) {
   switch (best) {
     case 0: launch_tile<Y, 2, 1, 1, 4, 4>(a, stream); break;
     case 1: launch_tile<Y, 2, 1, 2, 4, 4>(a, stream); break;
-    case 2: launch_tile<Y, 4, 1, 2, 4, 4>(a, stream); break;
-    case 3: launch_tile<Y, 4, 2, 2, 4, 4>(a, stream); break;
-    case 4: launch_tile<Y, 4, 4, 2, 4, 3>(a, stream); break;
+    case 2: launch_tile<Y, 2, 2, 2, 4, 4>(a, stream); break;
+    case 3: launch_tile<Y, 4, 1, 2, 4, 4>(a, stream); break;
+    case 4: launch_tile<Y, 4, 2, 2, 4, 4>(a, stream); break;
+    case 5: launch_tile<Y, 4, 4, 2, 4, 3>(a, stream); break;
     default: launch_tile<Y, 8, 4, 2, 4, 2>(a, stream); break;
   }
 }
