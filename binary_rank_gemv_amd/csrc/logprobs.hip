@@ -171,6 +171,11 @@ __device__ __forceinline__ void tops_flush(Tops& T, u64* buf, int top, int lane,
   T.least = lane_of(T.list, top - 1);
 }
 
+// v[i] for an i of the lane's own: all in registers (out of an array the compiler
+// makes an indexed read of scratch memory of it).
+typedef float f32xe __attribute__((ext_vector_type(kEpt)));
+__device__ __forceinline__ float pick(f32xe v, int i) { return v[i]; }
+
 // Collects the chunk's logits of at least `floor` (NaN: all) that can be among
 // the `top` largest.  `v` holds kEpt of them, the first `valid` inside the row;
 // place(i) is where the i-th stands.
@@ -178,15 +183,15 @@ template <typename PLACE>
 __device__ __forceinline__ void tops_chunk(Tops& T, u64* buf, int top, int lane, const float (&v)[kEpt], int valid,
                                            float floor, PLACE place) {
   uint32_t todo = 0;
+  f32xe all;
 #pragma unroll
-  for (int i = 0; i < kEpt; ++i)
+  for (int i = 0; i < kEpt; ++i) {
+    all[i] = v[i];
     if (i < valid && !(v[i] < floor)) todo |= 1u << i;
+  }
   while (__ballot(todo != 0) != 0) {
     const int i = todo ? __builtin_ctz(todo) : 0;
-    float x = v[0];
-#pragma unroll
-    for (int j = 1; j < kEpt; ++j) x = i == j ? v[j] : x;
-    const u64 k = key_of(x, place(i));
+    const u64 k = key_of(pick(all, i), place(i));
     const bool in = todo && k > T.least;
     const u64 ins = __ballot(in);
     if (in) buf[T.pending + __popcll(ins & ((1ull << lane) - 1))] = k;
