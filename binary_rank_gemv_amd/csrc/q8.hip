@@ -278,7 +278,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void lb_q8_stream_kernel(const L
 //
 // What bounds it: 256 x 256 tiles run the matrix units 56% of the time at
 // 1.9 GHz, the clock that the card's power leaves for random codes (2000 x 4096 ->
-// 32000: 242 us, 2.17 POP/s; the vendor's int8 product of 8192 cubed reaches
+// 32000: 250 us, 2.1 POP/s; the vendor's int8 product of 8192 cubed reaches
 // 2.07).  The smaller tiles are bound by what a compute unit loads, about 50
 // bytes a ns, and by their start and end of about 5 us.
 struct TileAt {

@@ -127,7 +127,8 @@ lb_status littlebit_q8_linear_fwd(const int8_t *xq, int64_t ldx, const float *xs
  *   lse       fp32 [2][rows]: the row's maximum m, then log sum exp(x - m);
  *             lse is their sum.  (Apart, so that nothing is lost where the
  *             logits lie far from 0, as in a row masked with the type's
- *             lowest value.)
+ *             lowest value.)  A row of -infinity has the lowest fp32 value and
+ *             -infinity.
  *   top       0 <= top <= min(vocab, LB_TOP_MAX); top_logprob fp32 and
  *             top_index int64, rows x top each, contiguous; NULL for top = 0.
  *   ws        littlebit_logprobs_workspace_bytes(rows, vocab, dtype, top)

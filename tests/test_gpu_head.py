@@ -539,6 +539,27 @@ def test_many_rows(head):
     assert torch.equal(x[-1:], head.littlebit_logprobs_bwd(last, targets[-1:], b[2], b[1], one[:1], one[:1]))
 
 
+def test_the_longest_row(head):
+    """2^30 logits in a row: split over 512 workgroups, 8192 of them a thread."""
+    case("the longest row")
+    vocab = 1 << 30
+    x = torch.empty(1, vocab, dtype=torch.float16, device="cuda").normal_()
+    x[0, 123_456_789], x[0, vocab - 1], x[0, 77] = 30.0, 31.0, -np.inf
+    total = torch.zeros((), dtype=torch.float64, device="cuda")
+    for part in x[0].split(1 << 26):
+        total += part.double().sub_(31).exp_().sum()
+    lse = 31 + float(total.log())
+    lp, H, parts, tv, ti = head.littlebit_logprobs_fwd(x, torch.tensor([vocab - 1], device="cuda"), 2)
+    assert ti.tolist() == [[vocab - 1, 123_456_789]]
+    tol = (8192 + 100) * 2 * U + 4 * U * 31
+    assert abs(float(parts.sum()) - lse) <= tol and abs(float(lp) - (31 - lse)) <= tol
+    assert abs(float(tv[0, 1]) - (30 - lse)) <= tol
+    x.fill_(1.0)                      # all equal: the lowest places, 30 log 2
+    lp, H, parts, tv, ti = head.littlebit_logprobs_fwd(x, torch.tensor([5], device="cuda"), 2)
+    assert ti.tolist() == [[0, 1]]
+    assert abs(float(lp) + 30 * np.log(2)) <= 2 * tol and abs(float(H) - 30 * np.log(2)) <= 2 * tol
+
+
 # ------------------------------------------------------------------------------------------------------- together
 
 def _model(head, n=512, vocab=2000, seed=3):
