@@ -227,7 +227,10 @@ template <typename T, int G, int R, int V>
 __global__ __launch_bounds__(G * R) void lb_norm_bwd_kernel(const LbNormBwdArgs A) {
   constexpr int kW = G / 64;
   constexpr bool kAhead = V == 1;  // registers for the next row
-  constexpr bool kInLds = V == 4;  // the columns' sums (128 KB) in LDS: no registers for them
+  // the longest rows: the columns' sums (128 KB) in LDS, no registers for them (512 x
+  // 32768: 70 us with both kernels, registers still spill; reading dhidden and the
+  // weight where they are used instead of holding them: 80)
+  constexpr bool kInLds = V == 4;
   __shared__ float part[2][2][R][kW];
   __shared__ float join[kInLds ? G * V * 8 : R > 1 ? (R - 1) * G * V * 8 : 1];
   const int t = threadIdx.x % G, rg = threadIdx.x / G, w = wave_id() % kW, lane = threadIdx.x & 63;
