@@ -198,9 +198,10 @@ lb_status littlebit_q8_linear_fwd(const int8_t* xq, int64_t ldx, const float* xs
 }
 
 size_t littlebit_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int dtype, int top) {
+  if (dtype != LB_F32 && dtype != LB_F16 && dtype != LB_BF16) return 0;
   if (rows < 1 || rows > kMaxRows || vocab < 1 || vocab > kMaxVocab || top < 0 || top > LB_TOP_MAX) return 0;
   int span = 0;
-  return lb_logprobs_partial_bytes(rows, lb_logprobs_splits(rows, vocab, dtype, &span), top);
+  return lb_logprobs_partial_bytes(rows, lb_logprobs_splits(rows, vocab, &span), top);
 }
 
 lb_status littlebit_logprobs_fwd(const void* logits, int64_t ld, int dtype, int64_t rows, int64_t vocab,
@@ -226,7 +227,7 @@ lb_status littlebit_logprobs_fwd(const void* logits, int64_t ld, int dtype, int6
     LB_TRY(check_vector(name, "top_index", top_index, 8));
   }
   LbLogprobsArgs a = {};
-  a.splits = lb_logprobs_splits(rows, vocab, dtype, &a.span);
+  a.splits = lb_logprobs_splits(rows, vocab, &a.span);
   LB_TRY(check_workspace(name, ws, ws_bytes, lb_logprobs_partial_bytes(rows, a.splits, top)));
   a.logits = logits; a.ld = ld;
   a.targets = targets;

@@ -77,7 +77,7 @@ hipError_t lb_launch_norm(const LbNormArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_norm_bwd(const LbNormBwdArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_q8_quantize(const LbNormArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_q8_linear(const LbQ8LinearArgs& a, int y_dtype, hipStream_t stream);
-int lb_logprobs_splits(int64_t rows, int64_t vocab, int dtype, int* span);
+int lb_logprobs_splits(int64_t rows, int64_t vocab, int* span);
 size_t lb_logprobs_partial_bytes(int64_t rows, int splits, int top);
 hipError_t lb_launch_logprobs(const LbLogprobsArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_logprobs_bwd(const LbLogprobsBwdArgs& a, int dtype, hipStream_t stream);

@@ -596,8 +596,7 @@ void launch_bwd(const LbLogprobsBwdArgs& a, hipStream_t stream) {
 // into parts of two chunks at least while the card has fewer than 512
 // workgroups (1 x 128256 bf16 with 5 alternatives: 26.8 us whole, 10.9 in 8;
 // 61 x 100003 with 20: 23.9 and 14.4; 512 x 128256: 37.8, and 35.5 in 2).
-int lb_logprobs_splits(int64_t rows, int64_t vocab, int dtype, int* span) {
-  (void)dtype;
+int lb_logprobs_splits(int64_t rows, int64_t vocab, int* span) {
   const int64_t chunks = (vocab + kChunk - 1) / kChunk;
   int64_t splits = rows > 0 && chunks > 16 ? 512 / rows : 1;
   if (splits > (chunks + 1) / 2) splits = (chunks + 1) / 2;
