@@ -92,6 +92,26 @@ def test_norm_forward(head, rows, n, dt):
         assert (np.abs(codes - want / s[:, None]) <= 0.5 + 127 * err).all()
 
 
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_norm_codes_are_the_exact_quotients_rounded(head, dt):
+    """The products h w and their largest are exact in fp32, so the codes are those of
+    the exact quotients.  The kernel decides by a remainder of at most 1/2 that is rounded
+    twice, 2 * 2^-26 = 3e-8 of a step: quotients within 1e-7 of a half are left out."""
+    case("norm codes", dt)
+    t = TYPES[dt]
+    x, w = randn(5, 300, 5000).to(t), (1 + 0.3 * randn(6, 5000)).to(t)
+    q, _, _ = head.littlebit_rmsnorm_q8(x.cuda(), w.cuda())
+    hw = f64(x) * f64(w)
+    want = 127 * hw / np.abs(hw).max(1, keepdims=True)
+    clear = np.abs(np.abs(want - np.trunc(want)) - 0.5) > 1e-7
+    assert clear.mean() > 0.999
+    assert np.array_equal(f64(q)[clear], np.rint(want)[clear])
+    q, _ = head.littlebit_q8_quantize(x.float().cuda())
+    want = 127 * f64(x) / np.abs(f64(x)).max(1, keepdims=True)
+    clear = np.abs(np.abs(want - np.trunc(want)) - 0.5) > 1e-7
+    assert np.array_equal(f64(q)[clear], np.rint(want)[clear])
+
+
 def test_norm_rows_of_zeros_nan_and_infinity(head):
     case("norm special rows")
     x = torch.ones(5, 300, dtype=torch.float16)
