@@ -85,6 +85,19 @@ __device__ __forceinline__ void group_reduce(float& s, float& a) {
   }
 }
 
+// The power of two that a row is multiplied by where its sum of squares leaves the
+// range of fp32 (values of bf16 beyond some 1e19; below 1e-14, where eps does not
+// cover them): y = h r has none of it, and the sums are formed again. The question
+// costs 0.2 us of 2047 x 8192 forward and some 0.6 of 2048 x 4096 backward (15.8, now 16.4).
+template <typename T>
+__device__ __forceinline__ float row_power(float s2, float eps) {
+  if constexpr (__is_same(T, bf16)) {
+    if (s2 == INFINITY) return 0x1p-80f;
+    if (s2 < 0x1p-90f && eps < 0x1p-100f) return 0x1p70f;
+  }
+  return 1.0f;
+}
+
 // QUANT: the row quantiser alone (no residual, weight or norm).
 template <typename T, int G, int V, bool QUANT>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNormArgs A) {
@@ -142,7 +155,33 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNorm
   }
   group_reduce<G>(s2, a);
   float r = 1.0f;
-  if constexpr (!QUANT) r = 1.0f / sqrtf(s2 / (float)A.n + A.eps);
+  if constexpr (!QUANT) {
+    float eps = A.eps;
+    const float up = row_power<T>(s2, eps);
+    if (up != 1.0f) {  // all threads of the row
+      const T* hp = A.hidden ? (const T*)A.hidden + row * A.ldh : x;
+      eps = eps * up * up;  // in this order: up^2 alone can leave the range
+      s2 = a = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int k = 8 * (t + i * G);
+        const long left = A.n - k;
+        float wt[8];
+        load8(hp + k, left > 0 ? left : 0, 0.0f, h[i]);
+        load8((const T*)A.weight + k, left > 0 ? left : 0, 0.0f, wt);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float he = h[i][e] * up;
+          hw[i][e] = he * wt[e];
+          s2 += he * he;
+          a = fmaxf(a, fabsf(hw[i][e]));
+        }
+      }
+      if constexpr (G > 64) __syncthreads();  // the first sums have been read
+      group_reduce<G>(s2, a);
+    }
+    r = 1.0f / sqrtf(s2 / (float)A.n + eps);
+  }
   const float top = QUANT ? a + s2 : a * r;  // s2 is 0 or NaN for the quantiser
   fine = top < INFINITY;                     // false for NaN too
   if (A.q) {
@@ -207,7 +246,7 @@ void launch_norm(const LbNormArgs& a, hipStream_t stream) {
 // sum of its columns over its rows in registers, the R rows that a workgroup
 // holds at a time join theirs in LDS at the end, and a second kernel adds the
 // workgroups, all in a fixed order.  The next row's loads are under way while a
-// row is reduced.  2048 x 4096 bf16: 14.8 us (4.8 TB/s with the partial sums) and 2
+// row is reduced.  2048 x 4096 bf16: 15.0 us (4.7 TB/s with the partial sums) and 2
 // to 4 for the sum of the workgroups; with one row at a time and twice the
 // workgroups it was 16.6 and 5.2.
 template <typename T, int V>
@@ -230,6 +269,11 @@ __device__ __forceinline__ float part_of(const u32x4& w, int e) {
   return e & 1 ? Pair<T>::hi(w[e >> 1]) : Pair<T>::lo(w[e >> 1]);
 }
 
+// A value that all lanes of the wave hold.
+__device__ __forceinline__ float wave_value(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+
 template <typename T, int G, int R, int V>
 __global__ __launch_bounds__(G * R) void lb_norm_bwd_kernel(const LbNormBwdArgs A) {
   constexpr int kW = G / 64;
@@ -238,7 +282,7 @@ __global__ __launch_bounds__(G * R) void lb_norm_bwd_kernel(const LbNormBwdArgs 
   // 32768: 70 us with both kernels, registers still spill; reading dhidden and the
   // weight where they are used instead of holding them: 80)
   constexpr bool kInLds = V == 4;
-  __shared__ float part[2][2][R][kW];
+  __shared__ float part[3][2][R][kW];  // two in turn, one for rows out of range
   __shared__ float join[kInLds ? G * V * 8 : R > 1 ? (R - 1) * G * V * 8 : 1];
   const int t = threadIdx.x % G, rg = threadIdx.x / G, w = wave_id() % kW, lane = threadIdx.x & 63;
   u32x4 wt[V];
@@ -285,8 +329,8 @@ __global__ __launch_bounds__(G * R) void lb_norm_bwd_kernel(const LbNormBwdArgs 
     }
     s2 = wave_sum(s2);
     uh = wave_sum(uh);
+    [[maybe_unused]] const int flip = j & 1;
     if constexpr (kW > 1) {
-      const int flip = j & 1;
       if (lane == 0) {
         part[flip][0][rg][w] = s2;
         part[flip][1][rg][w] = uh;
@@ -300,8 +344,55 @@ __global__ __launch_bounds__(G * R) void lb_norm_bwd_kernel(const LbNormBwdArgs 
         uh += part[flip][1][rg][i];
       }
     }
-    const float r = 1.0f / sqrtf(s2 / (float)A.n + A.eps);
-    const float c = (uh * r) * r / (float)A.n;
+    const float up = wave_value(row < A.rows ? row_power<T>(s2, A.eps) : 1.0f);
+    if constexpr (__is_same(T, bf16)) {
+      bool again = up != 1.0f;
+      if constexpr (R > 1 && kW > 1) {
+        // the same answer in the whole workgroup, for the barrier: from all its waves' sums,
+        // sixteen at most to a row (a row that is in range has the same sums again)
+        const float q = lane < R * kW ? part[flip][0][lane / kW][lane % kW] : 1.0f;
+        again = __ballot(!(q < 0x1p120f) || (q < 0x1p-90f && A.eps < 0x1p-100f)) != 0;
+      }
+      if (again) {
+        s2 = uh = 0.0f;
+        auto add = [&](const u32x4& hv, const u32x4& dyv, const u32x4& wv) __attribute__((always_inline)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float h = part_of<T>(hv, e) * up;
+            s2 += h * h;
+            uh += part_of<T>(wv, e) * part_of<T>(dyv, e) * h;
+          }
+        };
+        if constexpr (V < 4) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) add(in.h[i], in.dy[i], wt[i]);
+        } else {  // read again: the usual way needs the registers
+#pragma unroll 1
+          for (int k = 8 * t; k < A.n && row < A.rows; k += 8 * G) {
+            const long left = (long)A.n - k;
+            add(raw8((const T*)A.hidden + row * A.ldh + k, left), raw8((const T*)A.dy + row * A.lddy + k, left),
+                raw8((const T*)A.weight + k, left));
+          }
+        }
+        s2 = wave_sum(s2);
+        uh = wave_sum(uh);
+        if constexpr (kW > 1) {
+          if (lane == 0) {
+            part[2][0][rg][w] = s2;
+            part[2][1][rg][w] = uh;
+          }
+          __syncthreads();
+          s2 = uh = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kW; ++i) {
+            s2 += part[2][0][rg][i];
+            uh += part[2][1][rg][i];
+          }
+        }
+      }
+    }
+    const float ru = 1.0f / sqrtf(s2 / (float)A.n + A.eps * up * up), r = ru * up;
+    const float c = (uh * ru) / (float)A.n * r;
     const bool real = row < A.rows;  // behind the last row there are zeros; with eps = 0 their r is infinite
 #pragma unroll
     for (int i = 0; i < V; ++i) {

@@ -57,8 +57,9 @@ extern "C" {
  *   y         dense output, or NULL.
  *   q, scale  8-bit output (int8 and one fp32 scale a row), or both NULL.  At
  *             least one of y and q is given.  y and q overlap no input.
- * A row of zeros has scale 0 (eps > 0).  A row with a NaN or an infinity has scale NaN
- * and q 0.  1 <= n <= LB_NORM_MAX_N.
+ * A row of zeros has scale 0 (eps > 0; with eps = 0 its y is NaN).  A row with a
+ * NaN or an infinity has scale NaN and q 0.  Rows of any other size are normed, those
+ * whose squares fp32 does not hold (bf16) too.  1 <= n <= LB_NORM_MAX_N.
  */
 lb_status littlebit_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr,
                                 const void *weight, int dtype, int64_t rows, int64_t n, float eps,
@@ -78,6 +79,7 @@ lb_status littlebit_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual
  *   ws        littlebit_rmsnorm_bwd_workspace_bytes(rows, n) bytes, 16-byte
  *             aligned.
  * The sums over rows run in a fixed order: the same call gives the same bits.
+ * With eps = 0 every row needs a normal value of its type: r is held in fp32.
  */
 size_t littlebit_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t n);
 

@@ -112,6 +112,40 @@ def test_norm_codes_are_the_exact_quotients_rounded(head, dt):
     assert np.array_equal(f64(q)[clear], np.rint(want)[clear])
 
 
+@pytest.mark.parametrize("n", [40, 1000, 3000, 5000, 9001, 20000])
+@pytest.mark.parametrize("size,eps", [(1e25, 1e-5), (3e36, 1e-5), (1e-20, 0.0), (1e-37, 0.0)])
+def test_norm_rows_whose_squares_leave_fp32(head, n, size, eps):
+    """bf16 alone has such values; between them are ordinary rows, that keep their bits."""
+    case("norm out of range", n, size, eps)
+    t = torch.bfloat16
+    x, dy = randn(n, 700, n).to(t), randn(n + 1, 700, n).to(t)
+    plain = x.clone()
+    far = torch.arange(700) % 7 == 3
+    x[far] = (x[far].double() * size).to(t)
+    w = (1 + 0.2 * randn(n + 2, n)).to(t)
+    h, W, DY = f64(x), f64(w), f64(dy)
+    want = oh.rmsnorm(h, W, eps)
+    err = chain(n) * U
+    e = half_step(t)
+    y, _ = head.littlebit_rmsnorm_fwd(x.cuda(), w.cuda(), eps=eps)
+    assert (np.abs(f64(y) - want) <= (e + err * (1 + e)) * np.abs(want) + SUB[t]).all()
+    assert torch.equal(y[~far], head.littlebit_rmsnorm_fwd(plain.cuda(), w.cuda(), eps=eps)[0][~far])
+    q, scale, _ = head.littlebit_rmsnorm_q8(x.cuda(), w.cuda(), eps=eps)
+    s = oh.q8_scale(want)
+    assert (np.abs(f64(scale) - s) <= err * s).all()
+    assert (np.abs(f64(q) - want / s[:, None]) <= 0.5 + 127 * err).all()
+    dx, dw = head.littlebit_rmsnorm_bwd(dy.cuda(), x.cuda(), w.cuda(), eps=eps)
+    want_dx, want_dw = oh.rmsnorm_backward(DY, h, W, eps)
+    r = 1 / np.sqrt((h * h).mean(1, keepdims=True) + eps)
+    part = np.abs(h * r) * r * np.mean(np.abs(W * DY * (h * r)), 1, keepdims=True)
+    bound = (chain(n) + 8) * U * (r * np.abs(W * DY) + 2 * part)
+    held = np.abs(want_dx) < 1e38          # gradients beyond the type are infinite
+    off = np.abs(f64(dx) - want_dx) <= half_step(t) * (np.abs(want_dx) + bound) + bound + SUB[t]
+    assert off[held].all()
+    assert (np.abs(f64(dw) - want_dw) <= (700 + chain(n) + 64) * U * np.abs(DY * h * r).sum(0)).all()
+    assert torch.equal(dx[~far], head.littlebit_rmsnorm_bwd(dy.cuda(), plain.cuda(), w.cuda(), eps=eps)[0][~far])
+
+
 def test_norm_rows_of_zeros_nan_and_infinity(head):
     case("norm special rows")
     x = torch.ones(5, 300, dtype=torch.float16)
