@@ -392,7 +392,8 @@ class LittleBitHead:
         rows = x.shape[0]
         _vector("targets", targets, torch.int64, x.device, rows)
         vocab = self.linear.q.shape[0]
-        step = max(1, max_logit_bytes // (vocab * torch.empty((), dtype=dtype).element_size()))
+        step = max_logit_bytes // (vocab * torch.empty((), dtype=dtype).element_size())
+        step = min(max(1, step), 1 << 20)   # a call takes 2^21 rows at most
         parts = []
         for t in range(0, max(rows, 1), step):
             r = None if residual is None else residual[t:t + step]

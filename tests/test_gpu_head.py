@@ -676,6 +676,19 @@ def test_head_text_in_parts_is_the_text_at_once(head):
     assert e[0].shape == (0,) and e[3].shape == (0, 2)
 
 
+def test_head_text_of_more_tokens_than_a_call_takes(head):
+    rows = (1 << 21) + 5
+    case("long text", rows)
+    W, norm = randn(1, 6, 8).half().cuda(), torch.ones(8, dtype=torch.float16, device="cuda")
+    hd = head.LittleBitHead.from_weights(norm, W)
+    x = randn(2, 1000, 8).half().cuda()
+    targets = targets_of(3, 1000, 6).cuda()
+    at = torch.arange(rows, device="cuda") % 1000
+    lp, H, tv, ti = hd.logprobs(x[at], targets[at], top=2)
+    for got, want in zip((lp, H, tv, ti), hd.logprobs(x, targets, top=2)):
+        assert got.shape[0] == rows and torch.equal(got, want[at])
+
+
 def test_streams_and_graphs(head):
     """The chain captured once and replayed over new inputs, with the program's own
     eager work between the replays; two graphs share nothing."""
