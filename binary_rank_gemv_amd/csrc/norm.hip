@@ -17,36 +17,74 @@ namespace {
 
 constexpr float kBig = 0x1p100f;
 
-// 127 / a as a sum hi + lo, without leaving the range for a tiny a: values are
-// multiplied by `up` first (exact, a power of two).
+// What a row's codes rint(127 v / a) are formed with.  Where a is tiny or huge, values are
+// multiplied by `up` first (exact, a power of two), so that nothing leaves the range.
 struct Q8Scale {
-  float up, hi, lo;
+  float up, a, hi, lo;  // 127 / (a up) = hi + lo
 };
 __device__ __forceinline__ Q8Scale q8_scale(float a) {
   Q8Scale s;
-  s.up = a < 1e-30f ? kBig : 1.0f;
-  const float au = a * s.up;
+  s.up = a < 1e-30f ? kBig : a > 1e30f ? 1.0f / kBig : 1.0f;
+  s.a = a * s.up;
   // a row of zeros has codes 0
-  s.hi = (au > 0.0f && au < INFINITY) ? 127.0f / au : 0.0f;
-  s.lo = s.hi > 0.0f ? fmaf(-s.hi, au, 127.0f) / au : 0.0f;
+  s.hi = (s.a > 0.0f && s.a < INFINITY) ? 127.0f / s.a : 0.0f;
+  s.lo = s.hi > 0.0f ? fmaf(-s.hi, s.a, 127.0f) / s.a : 0.0f;
   return s;
 }
-// rint(127 v / a).  A product of two 2-byte values is exact in fp32, so v and a are;
-// what the quotient's rounding may have put on the wrong side of a half is seen
-// in the remainder (off by some 1e-8 of a step); a product with 127 / a alone takes
-// 25.3 of the 26.2 us above and puts a few codes in ten million on the other side.
-__device__ __forceinline__ int q8_code(float v, const Q8Scale& s) {
-  v *= s.up;
-  const float c = rintf(v * s.hi);
-  const float rest = fmaf(v, s.lo, fmaf(v, s.hi, -c));
-  return (int)fminf(fmaxf(c + rintf(rest), -127.0f), 127.0f);
+
+// Eight codes (their last 8 bits), those of the exact quotients, a half to the even code;
+// leaves v scaled by `up`.  A product of two 2-byte values is exact in fp32, so v and a
+// are.  A product with 127 / a alone would put a few codes in ten million on the other
+// side, and halves on either.
+template <bool SHORT>
+__device__ __forceinline__ void q8_codes(float (&v)[8], const Q8Scale& s, int (&c)[8]) {
+  if (s.up != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= s.up;
+  }
+  if constexpr (SHORT) {
+    // v has 17 bits at most: 127 v is exact, and so is the rest 127 v - c a, which is compared with
+    // a / 2 itself.  (Where c is 1 and the quotient below a half, the rest may be
+    // rounded to -a / 2, which gives code 0 too.)  Short values hit a half often.
+    const uint32_t half = __builtin_bit_cast(uint32_t, 0.5f * s.a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // rounded to a whole number by the addition, whose last bits are then the code's
+      const float near = fmaf(v[i], s.hi, 0x1.8p23f), rest = fmaf(0x1.8p23f - near, s.a, 127.0f * v[i]);
+      c[i] = __builtin_bit_cast(int, near);
+      // an odd code gives a half away: one unit less than a / 2 is allowed for it
+      const float most = __builtin_bit_cast(float, half - (uint32_t)(c[i] & 1));
+      const int step = __builtin_bit_cast(int, rest) >> 31 | 1;
+      c[i] += fabsf(rest) > most ? step : 0;
+    }
+  } else {
+    // the rest as a share of a, off by less than 2^-23: what is that near to a half (a few
+    // in a million, more where the weight is 1) is decided by 127 v - (c +- 1/2) a, exact in 64 bits
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = v[i], q = rintf(w * s.hi), rest = fmaf(w, s.lo, fmaf(w, s.hi, -q));
+      most = fmaxf(most, fabsf(rest));
+      c[i] = (int)(q + rintf(rest));
+    }
+    if (most > 0.5f - 0x1p-22f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = v[i], q = rintf(w * s.hi), rest = fmaf(w, s.lo, fmaf(w, s.hi, -q));
+        const bool above = rest > 0.0f;
+        const double off = fma(-(double)(q + (above ? 0.5f : -0.5f)), (double)s.a, 127.0 * (double)w);
+        c[i] = (int)q;
+        if (off == 0.0 ? (c[i] & 1) != 0 : (off > 0.0) == above) c[i] += above ? 1 : -1;
+      }
+    }
+  }
 }
 
 // `fine`: the row is finite (otherwise its codes are 0).
-__device__ __forceinline__ void q8_store(int8_t* p, long left, const float (&v)[8], const Q8Scale& s, bool fine) {
-  int c[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = fine ? q8_code(v[i], s) : 0;
+template <bool SHORT>
+__device__ __forceinline__ void q8_store(int8_t* p, long left, float (&v)[8], const Q8Scale& s, bool fine) {
+  int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (fine) q8_codes<SHORT>(v, s, c);
   if (left >= 8) {
     u32x2 w;
 #pragma unroll
@@ -184,16 +222,6 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNorm
   }
   const float top = QUANT ? a + s2 : a * r;  // s2 is 0 or NaN for the quantiser
   fine = top < INFINITY;                     // false for NaN too
-  if (A.q) {
-    const Q8Scale sc = q8_scale(a);
-    int8_t* qp = A.q + row * A.ldq;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int k = 8 * (t + i * G);
-      q8_store(qp + k, (long)A.n - k, hw[i], sc, fine);
-    }
-    if (t == 0) A.scale[row] = fine ? top / 127.0f : NAN;
-  }
   if constexpr (!QUANT) {
     if (A.y) {
       T* yp = (T*)A.y + row * A.ldy;
@@ -206,6 +234,17 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNorm
         store8(yp + k, (long)A.n - k, y);
       }
     }
+  }
+  if (A.q) {
+    const Q8Scale sc = q8_scale(a);
+    int8_t* qp = A.q + row * A.ldq;
+    constexpr bool kShort = sizeof(T) == 2 && (QUANT || __is_same(T, bf16));  // else 22 or 24 bits
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = 8 * (t + i * G);
+      q8_store<kShort>(qp + k, (long)A.n - k, hw[i], sc, fine);
+    }
+    if (t == 0) A.scale[row] = fine ? top / 127.0f : NAN;
   }
 }
 

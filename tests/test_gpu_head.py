@@ -112,6 +112,37 @@ def test_norm_codes_are_the_exact_quotients_rounded(head, dt):
     assert np.array_equal(f64(q)[clear], np.rint(want)[clear])
 
 
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_codes_of_quotients_that_are_halves_go_to_the_even_code(head, dt):
+    """Rows of multiples of half a step: every second quotient is a half.  127 v and a are exact
+    in float64, and their quotient, 31 by 24 bits, is a half or 2^-33 from one at least: the
+    reference's codes are exact, none is left out."""
+    case("codes of halves", dt)
+    t = TYPES[dt]
+    rng = np.random.default_rng(8)
+    half = torch.from_numpy(rng.integers(-254, 255, (500, 1000)) / 2.0)
+    half[:, 5] = 127.0
+    unit = torch.from_numpy(rng.integers(129, 256, (500, 1)) / 128.0)          # 8 bits
+    quotients = []
+    if dt == "fp32":
+        x = (half * unit).float()
+        quotients.append((x.double(), head.littlebit_q8_quantize(x.cuda())[0]))
+        x = randn(9, 500, 3000).float()
+        quotients.append((x.double(), head.littlebit_q8_quantize(x.cuda())[0]))
+    else:
+        x = half.to(t)
+        for i in range(0, 500, 50):
+            w = unit[i].expand(1000).to(t).contiguous()
+            quotients.append((x.double() * w.double(), head.littlebit_rmsnorm_q8(x.cuda(), w.cuda())[0]))
+        x = randn(9, 2000, 5000).to(t)
+        w = (1 + 0.3 * randn(10, 5000)).to(t)
+        quotients.append((x.double() * w.double(), head.littlebit_rmsnorm_q8(x.cuda(), w.cuda())[0]))
+    for v, q in quotients:
+        v = v.numpy()
+        want = np.rint(127 * v / np.abs(v).max(1, keepdims=True))
+        assert np.array_equal(f64(q), want)
+
+
 @pytest.mark.parametrize("n", [40, 1000, 3000, 5000, 9001, 20000])
 @pytest.mark.parametrize("size,eps", [(1e25, 1e-5), (3e36, 1e-5), (1e-20, 0.0), (1e-37, 0.0)])
 def test_norm_rows_whose_squares_leave_fp32(head, n, size, eps):
