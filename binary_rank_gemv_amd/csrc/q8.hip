@@ -445,12 +445,15 @@ __global__ __launch_bounds__(64 * MW * NW, 2) void lb_q8_tile_kernel(const LbQ8L
       products(a[I & 1], b[I & 1], 1);
       __builtin_amdgcn_sched_barrier(0);
     };
+    // a turn of the loop ends where the stages and the two register buffers both start again
+    constexpr int kTurn = ST % 2 ? 2 * ST : ST;
+    static_assert(kTurn % ST == 0 && kTurn % 2 == 0, "chunk c is in stage c % ST and in registers c % 2");
     for (int i = 0; i < ST; ++i) issue(i, stage(i));
     sync(std::integral_constant<int, ST - 1>());
     read(stage0, a[0], b[0]);
     int c = 0;
-    for (; c + ST <= C; c += ST) chunks_while(body, c, c + ST, std::make_integer_sequence<int, ST>());
-    chunks_while(body, c, C, std::make_integer_sequence<int, ST - 1>());
+    for (; c + kTurn <= C; c += kTurn) chunks_while(body, c, c + kTurn, std::make_integer_sequence<int, kTurn>());
+    chunks_while(body, c, C, std::make_integer_sequence<int, kTurn - 1>());
   }
   if (A.n & 127) {
     // the last inputs, straight from memory
@@ -569,10 +572,10 @@ void launch_few(const LbQ8LinearArgs& a, int ncu, hipStream_t stream) {
 // The tile shape whose rounds of workgroups over the compute units take the
 // least, counted in hundredths of a us a chunk as measured with one workgroup
 // a compute unit.  Against all shapes on fourteen sizes (24 to 2000 tokens, 4096 to
-// 32000 channels) this choice was the fastest or within 4%: 64 x 5120 -> 32000 in
-// 128 x 64 35 us (64 x 64 41, 128 x 128 38), 300 x 5120 -> 5120 in 64 x 128 18 (22, 26),
-// 201 x 5120 -> 13824 in 128 x 128 31 (64 x 128 38, 128 x 256 44), 512 x 4096 -> 11008 in
-// 128 x 256 33 (128 x 128 44, 256 x 256 57).
+// 32000 channels, weights from HBM) this choice was the fastest or within 4%: 64 x 5120 ->
+// 32000 in 128 x 64 36 us (64 x 64 41, 128 x 128 38), 300 x 5120 -> 5120 in 64 x 128 18 (22,
+// 26), 201 x 5120 -> 13824 in 128 x 128 31 (64 x 128 38, 128 x 256 44), 512 x 4096 -> 11008
+// in 128 x 256 35 (128 x 128 45, 64 x 128 47, 256 x 256 58).
 template <typename Y>
 void launch_linear(const LbQ8LinearArgs& a, hipStream_t stream) {
   const int ncu = cu_count();
