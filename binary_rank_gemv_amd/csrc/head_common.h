@@ -148,13 +148,15 @@ __device__ __forceinline__ float wave_sum(float v) {
   v += lane_xor<16>(v);
   return v + lane_xor<32>(v);
 }
+// The larger value, NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, lane_xor<1>(v));
-  v = fmaxf(v, lane_xor<2>(v));
-  v = fmaxf(v, lane_xor<4>(v));
-  v = fmaxf(v, lane_xor<8>(v));
-  v = fmaxf(v, lane_xor<16>(v));
-  return fmaxf(v, lane_xor<32>(v));
+  v = max_nan(v, lane_xor<1>(v));
+  v = max_nan(v, lane_xor<2>(v));
+  v = max_nan(v, lane_xor<4>(v));
+  v = max_nan(v, lane_xor<8>(v));
+  v = max_nan(v, lane_xor<16>(v));
+  return max_nan(v, lane_xor<32>(v));
 }
 
 }  // namespace lbh

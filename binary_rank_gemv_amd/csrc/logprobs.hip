@@ -41,8 +41,6 @@ constexpr int kWork = 256;                  // entries of the second look's list
 
 typedef unsigned long long u64;
 
-__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
-
 // exp(d) for d <= 0; a d of -infinity or below any representable exp gives 0
 __device__ __forceinline__ float exp_of(float d) { return __builtin_amdgcn_exp2f(d * kLog2e); }
 

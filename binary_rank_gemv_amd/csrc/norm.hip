@@ -100,7 +100,7 @@ __device__ __forceinline__ void q8_store(int8_t* p, long left, float (&v)[8], co
 }
 
 // Sum of `s` and maximum of `a` over a group of G threads (G = 64: a wave;
-// otherwise the whole workgroup).  A NaN in the row is in the sum.
+// otherwise the whole workgroup).  A NaN reaches the sum and the maximum.
 template <int G>
 __device__ __forceinline__ void group_reduce(float& s, float& a) {
   s = wave_sum(s);
@@ -118,7 +118,7 @@ __device__ __forceinline__ void group_reduce(float& s, float& a) {
 #pragma unroll
     for (int i = 1; i < G / 64; ++i) {
       s += part[0][i];
-      a = fmaxf(a, part[1][i]);
+      a = max_nan(a, part[1][i]);
     }
   }
 }
@@ -146,7 +146,6 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNorm
   const T* x = (const T*)A.x + row * A.ldx;
   float h[V][8], hw[V][8];
   float s2 = 0.0f, a = 0.0f;
-  bool fine = true;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int k = 8 * (t + i * G);
@@ -173,12 +172,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNorm
     for (int e = 0; e < 8; ++e) {
       if constexpr (QUANT) {
         hw[i][e] = h[i][e];
-        s2 += h[i][e] * 0.0f;  // NaN where the row has a NaN or an infinity
       } else {
         hw[i][e] *= h[i][e];
         s2 += h[i][e] * h[i][e];
       }
-      a = fmaxf(a, fabsf(hw[i][e]));
+      a = max_nan(a, fabsf(hw[i][e]));
     }
   }
   if constexpr (!QUANT) {
@@ -212,7 +210,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNorm
           const float he = h[i][e] * up;
           hw[i][e] = he * wt[e];
           s2 += he * he;
-          a = fmaxf(a, fabsf(hw[i][e]));
+          a = max_nan(a, fabsf(hw[i][e]));
         }
       }
       if constexpr (G > 64) __syncthreads();  // the first sums have been read
@@ -220,8 +218,9 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void lb_norm_kernel(const LbNorm
     }
     r = 1.0f / sqrtf(s2 / (float)A.n + eps);
   }
-  const float top = QUANT ? a + s2 : a * r;  // s2 is 0 or NaN for the quantiser
-  fine = top < INFINITY;                     // false for NaN too
+  // NaN where the row or the weight has one, or an infinity meets a 0
+  const float top = QUANT ? a : a * r;
+  const bool fine = top < INFINITY;  // false for NaN too
   if constexpr (!QUANT) {
     if (A.y) {
       T* yp = (T*)A.y + row * A.ldy;

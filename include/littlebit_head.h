@@ -58,8 +58,10 @@ extern "C" {
  *   q, scale  8-bit output (int8 and one fp32 scale a row), or both NULL.  At
  *             least one of y and q is given.  y and q overlap no input.
  * A row of zeros has scale 0 (eps > 0; with eps = 0 its y is NaN).  A row with a
- * NaN or an infinity has scale NaN and q 0.  Rows of any other size are normed, those
- * whose squares fp32 does not hold (bf16) too.  1 <= n <= LB_NORM_MAX_N.
+ * NaN or an infinity in h or in a weighted value h_j * weight_j has scale NaN and q 0.
+ * Rows of any other size are normed, those whose squares fp32 does not hold (bf16) too.
+ * (h_j * weight_j is formed in fp32 first: of fp16 values it always fits, of bf16
+ * ones it does for weights below 1e19.)  1 <= n <= LB_NORM_MAX_N.
  */
 lb_status littlebit_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr,
                                 const void *weight, int dtype, int64_t rows, int64_t n, float eps,

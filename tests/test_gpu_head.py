@@ -198,6 +198,30 @@ def test_norm_rows_of_zeros_nan_and_infinity(head):
     assert h.isinf().all() and scale.isnan().all()
 
 
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("n", [300, 2000, 5000, 9000, 20000])
+def test_norm_of_a_weight_with_nan_or_infinity(head, n, dt):
+    """A product h w that is NaN or infinite leaves no finite scale, wherever in the row it is,
+    and the dense output holds it."""
+    case("norm weight special", n, dt)
+    t = TYPES[dt]
+    x = randn(n, 4, n).to(t)
+    for place in (0, n // 2, n - 1):
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            x[:, place] = torch.tensor([1.0, 0.0, -2.0, 0.0])
+            w = torch.ones(n, dtype=t)
+            w[place] = bad
+            q, scale, _ = head.littlebit_rmsnorm_q8(x.cuda(), w.cuda())
+            y, _ = head.littlebit_rmsnorm_fwd(x.cuda(), w.cuda())
+            assert scale.isnan().all() and (q == 0).all()
+            with np.errstate(invalid="ignore"):
+                want = f64(x)[:, place] * bad
+            got = f64(y)[:, place]
+            assert np.array_equal(np.isnan(got), np.isnan(want)) and (got[~np.isnan(want)] == want[~np.isnan(want)]).all()
+            rest = torch.arange(n) != place
+            assert torch.isfinite(y.cpu()[:, rest]).all()
+
+
 def test_norm_hidden_in_place_and_untouched_surroundings(head):
     case("norm in place")
     t = torch.bfloat16
