@@ -399,6 +399,7 @@ class LittleBitHead:
             r = None if residual is None else residual[t:t + step]
             logits = self.logits(x[t:t + step], r, dtype, stream)
             logprob, entropy, _, values, places = littlebit_logprobs_fwd(logits, targets[t:t + step], top, stream)
+            del logits   # before the next part's are formed
             parts.append((logprob, entropy, values, places))
         if len(parts) == 1:
             return parts[0]

@@ -731,6 +731,25 @@ def test_head_text_in_parts_is_the_text_at_once(head):
     assert e[0].shape == (0,) and e[3].shape == (0, 2)
 
 
+def test_head_holds_one_part_of_the_logits(head):
+    case("head memory")
+    W, norm = randn(1, 32000, 64).half().cuda(), torch.ones(64, dtype=torch.float16, device="cuda")
+    hd = head.LittleBitHead.from_weights(norm, W)
+    x, targets = randn(2, 2500, 64).half().cuda(), targets_of(3, 2500, 32000).cuda()
+    room = 500 * 32000 * 4
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        hd.logprobs(x, targets, top=2, max_logit_bytes=room, stream=stream)
+        torch.cuda.synchronize()
+        # the allocator hands out large blocks whole, in steps of 2 MiB; besides the logits there are the codes, scales
+        # and lse of 500 tokens (64 + 4 + 8 bytes each) and the results of 2500 (32 bytes each): 118000 bytes, and less
+        # than 512 more for each of 25 tensors
+        block = -(-room // (2 << 20)) * (2 << 20)
+        assert torch.cuda.max_memory_allocated() - before <= block + (1 << 17)
+
+
 def test_head_text_of_more_tokens_than_a_call_takes(head):
     rows = (1 << 21) + 5
     case("long text", rows)
