@@ -389,8 +389,11 @@ class LittleBitHead:
         text of any length: the logits are formed for as many tokens at a time
         as fit in `max_logit_bytes`, and never kept.  The perplexity of the text is
         exp(-mean logprob)."""
-        rows = x.shape[0]
-        _vector("targets", targets, torch.int64, x.device, rows)
+        _, shape, device = _first("x", x, _HALF)
+        rows = shape[0]
+        if residual is not None:   # whole: a part of a longer one would fit its part of x
+            _matrix("residual", residual, x.dtype, device, shape)
+        _vector("targets", targets, torch.int64, device, rows)
         vocab = self.linear.q.shape[0]
         step = max_logit_bytes // (vocab * torch.empty((), dtype=dtype).element_size())
         step = min(max(1, step), 1 << 20)   # a call takes 2^21 rows at most

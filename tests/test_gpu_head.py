@@ -731,6 +731,19 @@ def test_head_text_in_parts_is_the_text_at_once(head):
     assert e[0].shape == (0,) and e[3].shape == (0, 2)
 
 
+def test_head_in_parts_refuses_a_residual_of_other_rows(head):
+    """Also where every part of the residual has its part's shape."""
+    case("head, other residuals")
+    W, norm, hd = _model(head)
+    x, targets = randn(4, 32, 512).half().cuda(), targets_of(1, 32, 2000).cuda()
+    for r in (x.repeat(2, 1), x[:16], x.repeat(1, 2)[:, :511], x.bfloat16(), x[0]):
+        with pytest.raises(ValueError):
+            hd.logprobs(x, targets, r, max_logit_bytes=2000 * 4 * 16)
+    for y in (x[0], x.float(), None):
+        with pytest.raises(ValueError):
+            hd.logprobs(y, targets)
+
+
 def test_head_holds_one_part_of_the_logits(head):
     case("head memory")
     W, norm = randn(1, 32000, 64).half().cuda(), torch.ones(64, dtype=torch.float16, device="cuda")
