@@ -388,7 +388,8 @@ class LittleBitHead:
         """(logprob, entropy, top_logprob, top_index) of the given tokens over a
         text of any length: the logits are formed for as many tokens at a time
         as fit in `max_logit_bytes`, and never kept.  The perplexity of the text is
-        exp(-mean logprob)."""
+        exp(-logprob[targets >= 0].mean()): tokens that are not given (negative
+        targets) have logprob 0 and are no part of the mean."""
         _, shape, device = _first("x", x, _HALF)
         rows = shape[0]
         if residual is not None:   # whole: a part of a longer one would fit its part of x

@@ -731,6 +731,20 @@ def test_head_text_in_parts_is_the_text_at_once(head):
     assert e[0].shape == (0,) and e[3].shape == (0, 2)
 
 
+def test_perplexity_of_a_padded_text(head):
+    """As the docstring has it: the same with padding as without."""
+    case("perplexity")
+    W, norm, hd = _model(head)
+    x, targets = randn(4, 40, 512).half().cuda(), torch.arange(40, device="cuda")
+    targets[25:] = -100
+    def perplexity(x, targets):
+        logprob = hd.logprobs(x, targets)[0]
+        return (-logprob[targets >= 0].mean()).exp()
+    # the logits of a row may be formed by another kernel (25 tokens or 40): the sums are exact, so the same bits
+    assert torch.equal(perplexity(x, targets), perplexity(x[:25], targets[:25]))
+    assert (hd.logprobs(x, targets)[0][25:] == 0).all()
+
+
 def test_head_in_parts_refuses_a_residual_of_other_rows(head):
     """Also where every part of the residual has its part's shape."""
     case("head, other residuals")
