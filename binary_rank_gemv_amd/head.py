@@ -16,7 +16,10 @@ the dense operators around the LittleBit layers, in ``_lib/liblittlebit_head.so`
 
 Work is enqueued on ``stream`` (default: the current stream of the tensors'
 device); the tensors of a call lie on one device, which need not be the
-current one.  Importing this module raises if the library has not been built
+current one.  Nothing is recorded for autograd: the backward passes are calls
+of their own, and while gradients are recorded a tensor that requires one is
+refused (call under ``torch.no_grad()``, as the methods of a
+``torch.autograd.Function`` are).  Importing this module raises if the library has not been built
 (``python -m binary_rank_gemv_amd.build``): there is no fallback path.
 """
 
@@ -140,6 +143,16 @@ def _table(name: str, t: torch.Tensor, dtype, device, shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+_recording = torch.is_grad_enabled
+
+
+def _no_history(*tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise ValueError("a tensor of the call requires a gradient, which would be lost: these calls record nothing for "
+                             "autograd; call under torch.no_grad() and take the gradient by the littlebit_*_bwd calls")
+
+
 def _new(rows: int, n: int, dtype, device) -> torch.Tensor:
     return _empty((rows, n), (n, 1), dtype=dtype, device=device)
 
@@ -167,6 +180,8 @@ def _norm(x, weight, residual, eps, hidden, dense, stream):
             ldh = _matrix("hidden", hidden, dtype, device, shape)
     elif hidden is not None:
         raise ValueError("hidden is an output of the residual's addition: give a residual")
+    if _recording():
+        _no_history(x, weight, residual, hidden)
     ctx, sp = _on(device, stream)
     with ctx:
         if residual is not None and hidden is None:
@@ -218,6 +233,8 @@ def littlebit_rmsnorm_bwd(dy: torch.Tensor, hidden: torch.Tensor, weight: torch.
     lddy = _matrix("dy", dy, dtype, device, shape)
     _vector("weight", weight, dtype, device, n)
     lddh = 0 if dhidden is None else _matrix("dhidden", dhidden, dtype, device, shape)
+    if _recording():
+        _no_history(dy, hidden, weight, dhidden)
     ctx, sp = _on(device, stream)
     with ctx:
         dx = _new(rows, n, dtype, device)
@@ -237,6 +254,8 @@ def littlebit_q8_quantize(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, t
     code, shape, device = _first("x", x, _DTYPE)
     ldx = _matrix("x", x, x.dtype, device, shape)
     rows, n = shape
+    if _recording():
+        _no_history(x)
     ctx, sp = _on(device, stream)
     with ctx:
         q, ldq = _codes(rows, n, device)
@@ -263,6 +282,8 @@ def littlebit_q8_linear_fwd(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Te
     code = _DTYPE.get(dtype)
     if code is None:
         raise ValueError("the output must be float32, float16 or bfloat16")
+    if _recording():
+        _no_history(xscale, wscale, out)
     ctx, sp = _on(device, stream)
     with ctx:
         y = out if out is not None else _new(batch, m, dtype, device)
@@ -285,6 +306,8 @@ def littlebit_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
     rows, vocab = shape
     if targets is not None:
         _vector("targets", targets, torch.int64, device, rows)
+    if _recording():
+        _no_history(logits)
     ctx, sp = _on(device, stream)
     with ctx:
         logprob = values = places = ws = None
@@ -337,6 +360,8 @@ def littlebit_logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
         _table("top_index", top_index, torch.int64, device, (rows, top))
         _table("dtop", dtop, torch.float32, device, (rows, top))
     ldd = vocab if out is None else _matrix("out", out, logits.dtype, device, shape)
+    if _recording():
+        _no_history(logits, lse, entropy, dlogprob, dentropy, dtop, out)
     ctx, sp = _on(device, stream)
     with ctx:
         d = _new(rows, vocab, logits.dtype, device) if out is None else out
@@ -358,8 +383,9 @@ class Q8Linear:
 
     @staticmethod
     def from_weight(weight: torch.Tensor) -> "Q8Linear":
-        """Quantises a dense m x n weight (fp32, fp16 or bf16, on the GPU)."""
-        return Q8Linear(*littlebit_q8_quantize(weight))
+        """Quantises a dense m x n weight (fp32, fp16 or bf16, on the GPU; a parameter's values)."""
+        with torch.no_grad():
+            return Q8Linear(*littlebit_q8_quantize(weight))
 
     def __call__(self, xq, xscale, dtype=torch.float16, out=None, stream=None) -> torch.Tensor:
         return littlebit_q8_linear_fwd(xq, xscale, self.q, self.scale, dtype, out, stream)
@@ -375,7 +401,7 @@ class LittleBitHead:
 
     @staticmethod
     def from_weights(norm: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5) -> "LittleBitHead":
-        return LittleBitHead(norm=norm, linear=Q8Linear.from_weight(weight), eps=eps)
+        return LittleBitHead(norm=norm.detach(), linear=Q8Linear.from_weight(weight), eps=eps)
 
     def logits(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, dtype=torch.float32,
                stream=None) -> torch.Tensor:

@@ -842,6 +842,56 @@ def test_streams_and_graphs(head):
     assert torch.equal(y, outs[0][0])
 
 
+def test_gradients_are_not_lost_in_silence(head):
+    """While autograd records, a tensor that requires a gradient is refused; without recording, and
+    inside a Function, the calls take it.  The Function's gradients are those of the formulas."""
+    case("requires grad")
+    x, r, w = randn(1, 6, 64).half().cuda(), randn(2, 6, 64).half().cuda(), (1 + 0.1 * randn(3, 64)).half().cuda()
+    lg, tg, f, g2 = randn(4, 6, 90).cuda(), torch.arange(6, device="cuda"), torch.rand(6, device="cuda"), torch.rand(6, 2, device="cuda")
+    lg = lg.float()
+    q, s = head.littlebit_q8_quantize(x)
+    lp, H, lse, tv, ti = head.littlebit_logprobs_fwd(lg, tg, 2)
+    calls = [(head.littlebit_rmsnorm_fwd, [x, w, r]), (head.littlebit_rmsnorm_q8, [x, w, r]),
+             (head.littlebit_rmsnorm_bwd, [x, r, w, x]), (head.littlebit_q8_quantize, [x]),
+             (head.littlebit_q8_linear_fwd, [q, s, q, s]), (head.littlebit_logprobs_fwd, [lg, tg, 2]),
+             (head.littlebit_logprobs_bwd, [lg, tg, lse, H, f, f, ti, g2])]
+    for call, args in calls:
+        want = call(*args)
+        for i, a in enumerate(args):
+            if not (torch.is_tensor(a) and a.is_floating_point()):
+                continue
+            leaf = [a.detach().clone().requires_grad_() if j == i else b for j, b in enumerate(args)]
+            with pytest.raises(ValueError, match="gradient"):
+                call(*leaf)
+            with torch.no_grad():
+                got = call(*leaf)
+            for p, q_ in zip(got if isinstance(got, tuple) else [got], want if isinstance(want, tuple) else [want]):
+                assert torch.equal(p, q_)
+    # a model's own parameters, without no_grad
+    hd = head.LittleBitHead.from_weights(torch.nn.Parameter(w), torch.nn.Parameter(lg[:, :64].half()))
+    assert hd.logprobs(x, tg, r)[0].shape == (6,)
+
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, residual, weight):
+            y, h = head.littlebit_rmsnorm_fwd(x, weight, residual)
+            ctx.save_for_backward(h, weight)
+            return y, h
+
+        @staticmethod
+        def backward(ctx, dy, dh):
+            h, weight = ctx.saved_tensors
+            dx, dw = head.littlebit_rmsnorm_bwd(dy.contiguous(), h, weight, dh.contiguous())
+            return dx, dx, dw.to(weight.dtype)
+
+    leaves = [t.detach().clone().requires_grad_() for t in (x, r, w)]
+    y, h = Norm.apply(*leaves)
+    dy, dh = randn(7, 6, 64).half().cuda(), randn(8, 6, 64).half().cuda()
+    torch.autograd.backward([y, h], [dy, dh])
+    dx, dw = head.littlebit_rmsnorm_bwd(dy, h.detach(), w, dh)
+    assert torch.equal(leaves[0].grad, dx) and torch.equal(leaves[1].grad, dx) and torch.equal(leaves[2].grad, dw.half())
+
+
 def test_refusals(head):
     case("refusals")
     x = torch.zeros(4, 64, dtype=torch.float16, device="cuda")
