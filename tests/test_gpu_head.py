@@ -266,6 +266,53 @@ def test_norm_backward(head, rows, n, dt):
         assert (np.abs(f64(dw) - want_dw) <= (rows + chain(n) + 64) * U * terms).all()
 
 
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,n", [(5, 300), (900, 1000), (600, 4000), (300, 5000), (3, 9000), (300, 20000)])
+def test_norm_to_both_outputs(head, rows, n, dt):
+    """y and q of one call are those of the two calls, ordinary rows and those out of range."""
+    case("norm, both outputs", rows, n, dt)
+    t = TYPES[dt]
+    x, r, w = randn(1, rows, n).to(t).cuda(), randn(2, rows, n).to(t).cuda(), (1 + 0.2 * randn(3, n)).to(t).cuda()
+    if dt == "bf16":
+        x[::3] *= 1e25
+        x[1::7] *= 1e35
+        r[1::7] = 0
+    y, h = head.littlebit_rmsnorm_fwd(x, w, r)
+    q, scale, _ = head.littlebit_rmsnorm_q8(x, w, r)
+    both = [torch.empty_like(h), torch.empty_like(y), torch.empty(rows, n, dtype=torch.int8, device="cuda"), torch.empty_like(scale)]
+    status = head.LIB.littlebit_rmsnorm_fwd(
+        x.data_ptr(), n, r.data_ptr(), n, w.data_ptr(), head._DTYPE[t], rows, n, 1e-5, both[0].data_ptr(), n,
+        both[1].data_ptr(), n, both[2].data_ptr(), n, both[3].data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    torch.cuda.synchronize()
+    for got, want in zip(both, (h, y, q, scale)):     # NaN where both factors reached a row
+        assert torch.allclose(got, want, rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,n", [(5, 300), (5000, 100), (3000, 1000), (1500, 4000), (700, 5000), (600, 9000), (600, 20000)])
+def test_norm_backward_in_place(head, rows, n, dt):
+    """dx may be dy, dhidden or hidden itself: many rows a workgroup, whose loads run ahead."""
+    case("norm backward in place", rows, n, dt)
+    t = TYPES[dt]
+    dy, dh, h = (torch.randn(rows, n, device="cuda").to(t) for _ in range(3))
+    if dt == "bf16":
+        h[::5] *= 1e25
+    w = (1 + 0.2 * randn(3, n)).to(t).cuda()
+    want, want_dw = head.littlebit_rmsnorm_bwd(dy, h, w, dh)
+    need = head.LIB.littlebit_rmsnorm_bwd_workspace_bytes(rows, n)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for place in range(3):
+        args = [t_.clone() for t_ in (dy, dh, h)]
+        dw = torch.empty(n, device="cuda")
+        status = head.LIB.littlebit_rmsnorm_bwd(
+            args[0].data_ptr(), n, args[1].data_ptr(), n, args[2].data_ptr(), n, w.data_ptr(), head._DTYPE[t], rows, n, 1e-5,
+            args[place].data_ptr(), n, dw.data_ptr(), ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+        torch.cuda.synchronize()
+        assert torch.equal(args[place], want) and torch.equal(dw, want_dw)
+
+
 def test_norm_backward_no_rows(head):
     case("norm backward of no rows")
     e = torch.empty(0, 50, dtype=torch.float16, device="cuda")
@@ -490,6 +537,29 @@ def test_logprobs_without_targets(head):
     a = head.littlebit_logprobs_fwd(x, None, 3)
     b = head.littlebit_logprobs_fwd(x, torch.zeros(4, dtype=torch.int64, device="cuda"), 3)
     assert a[0] is None and all(torch.equal(p, q) for p, q in zip(a[1:], b[1:]))
+
+
+@pytest.mark.parametrize("rows,vocab,top", [(5, 1000, 0), (3, 9001, 7), (2, 100003, 5)])
+def test_logprobs_without_entropy_or_targets(head, rows, vocab, top):
+    """What is not asked for is not written; the rest is the same."""
+    case("logprobs, NULL outputs", rows, vocab, top)
+    x, targets = randn(1, rows, vocab).half().cuda(), targets_of(2, rows, vocab).cuda()
+    want = head.littlebit_logprobs_fwd(x, targets, top)
+    need = head.LIB.littlebit_logprobs_workspace_bytes(rows, vocab, head._DTYPE[x.dtype], top)
+    for with_targets in (True, False):
+        lp, lse = torch.full((rows,), 7.0, device="cuda"), torch.empty(2, rows, device="cuda")
+        tv = torch.empty(rows, max(top, 1), device="cuda")
+        ti = torch.empty(rows, max(top, 1), dtype=torch.int64, device="cuda")
+        ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+        status = head.LIB.littlebit_logprobs_fwd(
+            x.data_ptr(), vocab, head._DTYPE[x.dtype], rows, vocab, targets.data_ptr() if with_targets else None,
+            lp.data_ptr() if with_targets else None, None, lse.data_ptr(), top, tv.data_ptr() if top else None,
+            ti.data_ptr() if top else None, ws.data_ptr() if need else None, need, torch.cuda.current_stream().cuda_stream)
+        assert status == 0
+        torch.cuda.synchronize()
+        assert torch.equal(lse, want[2]) and (torch.equal(lp, want[0]) if with_targets else (lp == 7).all())
+        if top:
+            assert torch.equal(tv, want[3]) and torch.equal(ti, want[4])
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
