@@ -22,8 +22,8 @@
  *
  * Matrices are row-major with a row stride (ld*, in elements) of at least the
  * row length.  Any alignment of a whole element is accepted; rows that start
- * at a multiple of 16 bytes are fastest.  `rows` may be 0 (nothing is
- * computed; a gradient summed over rows is then 0).
+ * at a multiple of 16 bytes are fastest.  `rows` (`batch`) may be 0 (nothing is
+ * computed; a gradient summed over rows is then 0) and is at most 2^21 a call.
  */
 #ifndef LITTLEBIT_HEAD_H
 #define LITTLEBIT_HEAD_H
@@ -82,6 +82,8 @@ lb_status littlebit_rmsnorm_fwd(const void *x, int64_t ldx, const void *residual
  *             aligned.
  * The sums over rows run in a fixed order: the same call gives the same bits.
  * With eps = 0 every row needs a normal value of its type: r is held in fp32.
+ * sum_i weight_i dy_i h_i has to stay in fp32's range (that of h / 2^80, where the
+ * squares of h do not).
  */
 size_t littlebit_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t n);
 
@@ -108,7 +110,7 @@ lb_status littlebit_q8_quantize(const void *x, int64_t ldx, int dtype, int64_t r
  *   xq        batch rows of n codes; wq m rows of n codes.
  *   xscale    fp32 [batch]; wscale fp32 [m].
  *   y         batch rows of m values, y_dtype LB_F32, LB_F16 or LB_BF16.
- * batch >= 0, m >= 1, 1 <= n <= 131071 (where 128^2 n stays below 2^31),
+ * batch >= 0, 1 <= m <= 2^24, 1 <= n <= 131071 (where 128^2 n stays below 2^31),
  * batch x m <= 2^38.
  */
 lb_status littlebit_q8_linear_fwd(const int8_t *xq, int64_t ldx, const float *xscale,
@@ -162,7 +164,9 @@ lb_status littlebit_logprobs_fwd(const void *logits, int64_t ld, int dtype, int6
  *   top_index, dtop     rows x top, contiguous; NULL for top = 0.
  *   lse, entropy, top_index  as littlebit_logprobs_fwd gave them.
  *   dlogits   the logits' type; may be the logits themselves (same stride).
- * The p_v terms of a masked logit are 0; a row of nothing else has gradient 0.
+ * The p_v terms of a masked logit are 0; a row of nothing else has gradient 0, whatever
+ * its target.
+ * rows x ceil(vocab / 8192) < 2^24.
  */
 lb_status littlebit_logprobs_bwd(const void *logits, int64_t ld, int dtype, int64_t rows,
                                  int64_t vocab, const int64_t *targets, const float *lse,
