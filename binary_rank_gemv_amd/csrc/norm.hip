@@ -7,7 +7,7 @@
 // exchange: the row is read once, held in registers, and the 8-bit codes need
 // no second reduction.  A group of G threads owns a row, thread t of it the
 // vectors t, t + G, ... of eight elements.  Memory bounds it: 2047 x 8192 bf16
-// with its residual, to 8 bits, 26.2 us (4.5 TB/s; a copy reaches 5.2).
+// with its residual, to 8 bits, 26.4 us in a replayed graph (4.4 TB/s; a copy reaches 5.2).
 #include "head_common.h"
 #include "head_launch.h"
 
@@ -126,7 +126,7 @@ __device__ __forceinline__ void group_reduce(float& s, float& a) {
 // The power of two that a row is multiplied by where its sum of squares leaves the
 // range of fp32 (values of bf16 beyond some 1e19; below 1e-14, where eps does not
 // cover them): y = h r has none of it, and the sums are formed again. The question
-// costs 0.2 us of 2047 x 8192 forward and some 0.6 of 2048 x 4096 backward (15.8, now 16.4).
+// costs 0.2 of the 26.4 us of 2047 x 8192 forward and 0.6 of the 17 of 2048 x 4096 backward.
 template <typename T>
 __device__ __forceinline__ float row_power(float s2, float eps) {
   if constexpr (__is_same(T, bf16)) {
@@ -255,8 +255,11 @@ void launch_one(const LbNormArgs& a, hipStream_t stream) {
 }
 
 // Threads a row by its length, and more of them, with fewer vectors each, while
-// there are few rows: one row of 5120 takes 5.3 us with 256 threads, 3.8 with 512,
-// 3.4 with 1024; 4096 rows take 38.8, 34.7 and 40.0.
+// there are few rows.  To 8 bits, bf16, one vector a thread against two: of 5120,
+// 1 row 3.8 and 4.0 us, 256 rows 5.4 and 5.9, 384 rows 7.4 and 7.2, 1024 rows 12.7 and
+// 12.1, 2048 rows 22.5 and 20.2; of 8192, 256 rows 6.2 and 6.4, 1024 rows 15.2 and 15.1,
+// 2048 rows 26.3 and 25.3; of 4096, 1 row 3.2 and 4.0, 512 rows 6.2 and 6.8, 1024 rows 9.8
+// and 9.9, 2048 rows 14.8 and 15.2 (dense 14.2 and 13.2).
 template <typename T, bool QUANT>
 void launch_norm(const LbNormArgs& a, hipStream_t stream) {
   if (a.n <= 512)
@@ -284,9 +287,9 @@ void launch_norm(const LbNormArgs& a, hipStream_t stream) {
 // sum of its columns over its rows in registers, the R rows that a workgroup
 // holds at a time join theirs in LDS at the end, and a second kernel adds the
 // workgroups, all in a fixed order.  The next row's loads are under way while a
-// row is reduced.  2048 x 4096 bf16: 15.0 us (4.7 TB/s with the partial sums) and 2
-// to 4 for the sum of the workgroups; with one row at a time and twice the
-// workgroups it was 16.6 and 5.2.
+// row is reduced.  2048 x 4096 bf16: 15.1 us (4.7 TB/s with the partial sums) and 3
+// to 4 for the sum of the workgroups in a kernel trace, both 17.0 in a replayed
+// graph; with one row at a time and twice the workgroups it was 16.6 and 5.2.
 template <typename T, int V>
 struct RowIn {
   u32x4 h[V], dy[V], dh[V];
@@ -558,7 +561,9 @@ hipError_t lb_launch_q8_quantize(const LbNormArgs& a, int dtype, hipStream_t str
   return hipGetLastError();
 }
 
-// Workgroups of the backward pass: one a compute unit, fewer for few rows.
+// Workgroups of the backward pass: one a compute unit of this architecture (a fixed
+// number, so that the sums and the workspace are the same on every part), fewer
+// for few rows.
 int lb_norm_bwd_groups(int64_t rows, int64_t n) {
   const int64_t r = bwd_shape(n).r, groups = (rows + r - 1) / r;
   return (int)(groups < 256 ? groups : 256);

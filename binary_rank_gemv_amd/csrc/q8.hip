@@ -577,7 +577,12 @@ void launch_few(const LbQ8LinearArgs& a, int ncu, hipStream_t stream) {
 // 32000 channels, weights from HBM) this choice was the fastest or within 4%: 64 x 5120 ->
 // 32000 in 128 x 64 36 us (64 x 64 41, 128 x 128 38), 300 x 5120 -> 5120 in 64 x 128 18 (22,
 // 26), 201 x 5120 -> 13824 in 128 x 128 31 (64 x 128 38, 128 x 256 44), 512 x 4096 -> 11008
-// in 128 x 256 35 (128 x 128 45, 64 x 128 47, 256 x 256 58).
+// in 128 x 256 35 (128 x 128 45, 64 x 128 47, 256 x 256 58).  Starts and ends, some 5 us a
+// shape, are not counted; on nine sizes with 256 or 512 inputs (64 to 2000 tokens, 5120 to
+// 32000 channels) the choice was the fastest all the same: 300 x 512 -> 5120 5.2 us in 64 x
+// 128 (128 x 64 5.3, 64 x 64 5.5).  Rows off 16 bytes are 1.3 to 2 times slower in all shapes
+// (201 x 5120 -> 13824 54 us, 2000 x 4096 -> 32000 319, against 31 and 245) and take the
+// same choice, there the fastest or within 6% on five sizes.
 template <typename Y>
 void launch_linear(const LbQ8LinearArgs& a, hipStream_t stream) {
   const int ncu = cu_count();
