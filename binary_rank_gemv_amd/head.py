@@ -15,8 +15,9 @@ the dense operators around the LittleBit layers, in ``_lib/liblittlebit_head.so`
   its 8-bit head, with the logits or the log probabilities of a text
 
 Work is enqueued on ``stream`` (default: the current stream of the tensors'
-device); the tensors of a call lie on one device, which need not be the
-current one.  Nothing is recorded for autograd: the backward passes are calls
+device), which the caller lets wait for what the tensors' own stream still
+writes; their memory is not reused before ``stream`` has passed the call.  The
+tensors of a call lie on one device, which need not be the current one.  Nothing is recorded for autograd: the backward passes are calls
 of their own, and while gradients are recorded a tensor that requires one is
 refused (call under ``torch.no_grad()``, as the methods of a
 ``torch.autograd.Function`` are).  Importing this module raises if the library has not been built
@@ -143,6 +144,14 @@ def _table(name: str, t: torch.Tensor, dtype, device, shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
+def _keep(stream, *tensors):
+    """Tensors that a call reads or writes on a stream given by name: freed ones are
+    not handed out again on their own stream while that one still runs."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 _recording = torch.is_grad_enabled
 
 
@@ -196,6 +205,8 @@ def _norm(x, weight, residual, eps, hidden, dense, stream):
             x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(), code, rows, n,
             eps, None if hidden is None else hidden.data_ptr(), ldh, None if y is None else y.data_ptr(), ldy,
             None if q is None else q.data_ptr(), ldq, None if scale is None else scale.data_ptr(), sp))
+    if stream is not None:
+        _keep(stream, x, weight, residual, hidden)
     return y, q, scale, x if residual is None else hidden
 
 
@@ -244,6 +255,8 @@ def littlebit_rmsnorm_bwd(dy: torch.Tensor, hidden: torch.Tensor, weight: torch.
         _check(LIB.littlebit_rmsnorm_bwd(
             dy.data_ptr(), lddy, None if dhidden is None else dhidden.data_ptr(), lddh, hidden.data_ptr(), ldh,
             weight.data_ptr(), code, rows, n, eps, dx.data_ptr(), n, dweight.data_ptr(), ws.data_ptr(), need, sp))
+    if stream is not None:
+        _keep(stream, dy, hidden, weight, dhidden)
     return dx, dweight
 
 
@@ -261,6 +274,8 @@ def littlebit_q8_quantize(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, t
         q, ldq = _codes(rows, n, device)
         scale = _empty((rows,), (1,), dtype=torch.float32, device=device)
         _check(LIB.littlebit_q8_quantize(x.data_ptr(), ldx, code, rows, n, q.data_ptr(), ldq, scale.data_ptr(), sp))
+    if stream is not None:
+        _keep(stream, x)
     return q, scale
 
 
@@ -289,6 +304,8 @@ def littlebit_q8_linear_fwd(xq: torch.Tensor, xscale: torch.Tensor, wq: torch.Te
         y = out if out is not None else _new(batch, m, dtype, device)
         _check(LIB.littlebit_q8_linear_fwd(xq.data_ptr(), ldx, xscale.data_ptr(), wq.data_ptr(), ldw,
                                            wscale.data_ptr(), batch, m, n, y.data_ptr(), ldy, code, sp))
+    if stream is not None:
+        _keep(stream, xq, xscale, wq, wscale, out)
     return y
 
 
@@ -326,6 +343,8 @@ def littlebit_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
             None if logprob is None else logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(), top,
             None if values is None else values.data_ptr(), None if places is None else places.data_ptr(),
             None if ws is None else ws.data_ptr(), need, sp))
+    if stream is not None:
+        _keep(stream, logits, targets)
     return logprob, entropy, lse, values, places
 
 
@@ -370,6 +389,8 @@ def littlebit_logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
             None if dentropy is None else entropy.data_ptr(), None if dlogprob is None else dlogprob.data_ptr(),
             None if dentropy is None else dentropy.data_ptr(), top, top_index.data_ptr() if top else None,
             dtop.data_ptr() if top else None, d.data_ptr(), ldd, sp))
+    if stream is not None:
+        _keep(stream, logits, targets, lse, entropy, dlogprob, dentropy, top_index, dtop, out)
     return d
 
 

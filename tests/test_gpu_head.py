@@ -912,6 +912,52 @@ def test_streams_and_graphs(head):
     assert torch.equal(y, outs[0][0])
 
 
+def test_tensors_freed_behind_a_call_on_another_stream(head):
+    """The caller's tensors go out of use as soon as the call returns, while the stream it was
+    given is still busy: what is allocated next does not take their memory."""
+    case("freed behind a stream")
+    rows, n, m = 64, 4096, 2048
+    made = lambda k, *shape: randn(k, *shape).half().cuda()  # noqa: E731
+    q, s = head.littlebit_q8_quantize(made(3, rows, n))
+    wq, ws = head.littlebit_q8_quantize(made(4, m, n))
+    lg, tg, f = made(5, rows, 9000), torch.arange(rows, device="cuda"), torch.rand(rows, device="cuda")
+    _, H, lse, _, _ = head.littlebit_logprobs_fwd(lg, tg)
+    calls = [(head.littlebit_rmsnorm_fwd, [made(0, rows, n), made(1, n), made(2, rows, n)]),
+             (head.littlebit_rmsnorm_q8, [made(0, rows, n), made(1, n), made(2, rows, n)]),
+             (head.littlebit_rmsnorm_bwd, [made(0, rows, n), made(2, rows, n), made(1, n), made(6, rows, n)]),
+             (head.littlebit_q8_quantize, [made(0, rows, n)]), (head.littlebit_q8_linear_fwd, [q, s, wq, ws]),
+             (head.littlebit_logprobs_fwd, [lg, tg]), (head.littlebit_logprobs_bwd, [lg, tg, lse, H, f, f])]
+    side = torch.cuda.Stream()
+    for call, args in calls:
+        want = call(*args)
+        want = want if isinstance(want, tuple) else (want,)
+        torch.cuda.synchronize()
+        temporary = [a.clone() for a in args]
+        sizes = [(a.shape, a.dtype) for a in args]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = call(*temporary, stream=side)
+        got = got if isinstance(got, tuple) else (got,)
+        del temporary
+        later = [torch.zeros(shape, dtype=t, device="cuda") for shape, t in sizes]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert (a is None and b is None) or torch.equal(a, b), call.__name__
+        del later, got
+        # the same captured, the stream named
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = call(*args, stream=side)
+        for _ in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(got if isinstance(got, tuple) else (got,), want):
+                assert (a is None and b is None) or torch.equal(a, b), call.__name__
+            torch.zeros(1 << 20, device="cuda").add_(1)
+        del graph, got
+
+
 def test_gradients_are_not_lost_in_silence(head):
     """While autograd records, a tensor that requires a gradient is refused; without recording, and
     inside a Function, the calls take it.  The Function's gradients are those of the formulas."""
