@@ -332,7 +332,7 @@ def littlebit_logprobs_fwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
             logprob = _empty((rows,), (1,), dtype=torch.float32, device=device)
         entropy = _empty((rows,), (1,), dtype=torch.float32, device=device)
         lse = _new(2, rows, torch.float32, device)
-        if top > 0:
+        if 0 < top <= LB_TOP_MAX:   # the call refuses others
             values = _new(rows, top, torch.float32, device)
             places = _new(rows, top, torch.int64, device)
         need = LIB.littlebit_logprobs_workspace_bytes(rows, vocab, code, top)
@@ -373,7 +373,7 @@ def littlebit_logprobs_bwd(logits: torch.Tensor, targets: Optional[torch.Tensor]
         _vector("dentropy", dentropy, torch.float32, device, rows)
     top = 0
     if dtop is not None:
-        if top_index is None or dtop.dim() != 2:
+        if top_index is None or not torch.is_tensor(dtop) or dtop.dim() != 2:
             raise ValueError("dtop needs top_index, one row of each a token")
         top = dtop.shape[1]
         _table("top_index", top_index, torch.int64, device, (rows, top))

@@ -912,6 +912,18 @@ def test_streams_and_graphs(head):
     assert torch.equal(y, outs[0][0])
 
 
+def test_alternatives_beyond_the_limit_take_no_memory(head):
+    case("refused top")
+    from binary_rank_gemv_amd.littlebit import LittleBitError
+    x = torch.zeros(2000, 300, dtype=torch.float16, device="cuda")
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    for top in (65, 300, 301, 1 << 30, (1 << 32) + 3):
+        with pytest.raises(LittleBitError):
+            head.littlebit_logprobs_fwd(x, None, top)
+    assert torch.cuda.max_memory_allocated() - before <= 2 * 2000 * 16    # entropy and lse, 12 bytes a row
+
+
 def test_tensors_freed_behind_a_call_on_another_stream(head):
     """The caller's tensors go out of use as soon as the call returns, while the stream it was
     given is still busy: what is allocated next does not take their memory."""
