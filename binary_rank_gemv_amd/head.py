@@ -17,10 +17,13 @@ the dense operators around the LittleBit layers, in ``_lib/liblittlebit_head.so`
 Work is enqueued on ``stream`` (default: the current stream of the tensors'
 device), which the caller lets wait for what the tensors' own stream still
 writes; their memory is not reused before ``stream`` has passed the call.  The
-tensors of a call lie on one device, which need not be the current one.  Nothing is recorded for autograd: the backward passes are calls
-of their own, and while gradients are recorded a tensor that requires one is
-refused (call under ``torch.no_grad()``, as the methods of a
-``torch.autograd.Function`` are).  Importing this module raises if the library has not been built
+tensors of a call lie on one device, which need not be the current one.
+
+Nothing is recorded for autograd: the backward passes are calls of their own,
+and while gradients are recorded a tensor that requires one is refused (call
+under ``torch.no_grad()``, as the methods of a ``torch.autograd.Function`` are).
+
+Importing this module raises if the library has not been built
 (``python -m binary_rank_gemv_amd.build``): there is no fallback path.
 """
 
