@@ -348,7 +348,7 @@ def _run_own(s):
                                                    s["k_weight"], **turn)
         return {"q_out": q, "k_out": k, "dq_in": dq, "dq_weight": dqw, "dk_in": dk, "dk_weight": dkw}
     cache = attn.LittleBitCache(s["k_pages"], s["v_pages"])
-    batch = attn.CacheBatch(s["starts"], s["lens"], s["table"], s["most"])
+    batch = attn.CacheBatch(s["starts"], s["lens"], s["table"])
     if s["op"] == "append":
         q = attn.littlebit_cache_append(cache, batch, s["k"], s["v"], s["q"], s["positions"], s["inv_freq"], s["q_weight"], s["k_weight"],
                                         eps=_EPS, interleaved=s["interleaved"])
