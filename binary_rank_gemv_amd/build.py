@@ -2,6 +2,11 @@
 
 * ``_lib/liblittlebit.so`` -- the layer (include/littlebit.h): packing,
   decode and prefill kernels, the C ABI.  Links only the HIP runtime.
+* ``_lib/liblittlebit_head.so`` -- the dense operators around the layers
+  (include/littlebit_head.h).  Links only the HIP runtime.
+* ``_lib/liblittlebit_attn.so`` -- what lies between a block's projections: head
+  norm and rotation, the paged cache and its attention
+  (include/littlebit_attn.h).  Links only the HIP runtime.
 * ``_lib/liblittlebit_init.so`` -- the offline Dual-SVID initialization
   (include/littlebit_init.h).  Links rocBLAS and rocSOLVER; the layer
   library does not depend on it.
@@ -28,6 +33,7 @@ OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "liblittlebit.so")
 INIT_LIB = os.path.join(LIBDIR, "liblittlebit_init.so")
 HEAD_LIB = os.path.join(LIBDIR, "liblittlebit_head.so")
+ATTN_LIB = os.path.join(LIBDIR, "liblittlebit_attn.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops keeps the compiler from emitting packed fp32 VALU forms.
@@ -40,10 +46,11 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 LAYER_SOURCES = ("decode.hip", "decode1.hip", "littlebit_host.hip", "pack.hip", "prefill.hip")
 INIT_SOURCES = ("init.hip",)
 HEAD_SOURCES = ("head_host.hip", "logprobs.hip", "norm.hip", "q8.hip")
+ATTN_SOURCES = ("attn.hip", "attn_host.hip", "heads.hip")
 
 
 def sources():
-    return [os.path.join(CSRC, f) for f in LAYER_SOURCES + INIT_SOURCES + HEAD_SOURCES]
+    return [os.path.join(CSRC, f) for f in LAYER_SOURCES + INIT_SOURCES + HEAD_SOURCES + ATTN_SOURCES]
 
 
 def _run(cmd, verbose):
@@ -111,23 +118,34 @@ def build_sanitized_host(verbose: bool = False) -> str:
 
 
 SANITIZED_HEAD_LIB = os.path.join(LIBDIR, "sanitized", "liblittlebit_head.so")
+SANITIZED_ATTN_LIB = os.path.join(LIBDIR, "sanitized", "liblittlebit_attn.so")
+
+
+def _build_sanitized(host_source, sources, out, verbose):
+    objdir = os.path.join(LIBDIR, "sanitized")
+    os.makedirs(objdir, exist_ok=True)
+    host = os.path.join(objdir, host_source + ".o")
+    _run([HIPCC, "--offload-arch=gfx950", "-O1", "-g", "-std=c++17", "-fPIC", "-c",
+          "-I", os.path.join(ROOT, "include"), "-I", CSRC, *DEVICE_FLAGS, *SANITIZE_HOST_FLAGS,
+          "-Xarch_host", "-fno-omit-frame-pointer", os.path.join(CSRC, host_source), "-o", host], verbose)
+    others = [os.path.join(OBJDIR, f + ".o") for f in sources if f != host_source]
+    missing = [o for o in others if not os.path.exists(o)]
+    if missing:
+        raise RuntimeError(f"build the library first; missing {missing}")
+    _link([host, *others], out, [*SANITIZE_HOST_FLAGS, "-shared-libsan"], verbose)
+    return out
 
 
 def build_sanitized_head(verbose: bool = False) -> str:
     """The same for the dense operators' library (head_host.hip); load it with
     LITTLEBIT_HEAD_LIBRARY=<path>."""
-    objdir = os.path.join(LIBDIR, "sanitized")
-    os.makedirs(objdir, exist_ok=True)
-    host = os.path.join(objdir, "head_host.hip.o")
-    _run([HIPCC, "--offload-arch=gfx950", "-O1", "-g", "-std=c++17", "-fPIC", "-c",
-          "-I", os.path.join(ROOT, "include"), "-I", CSRC, *DEVICE_FLAGS, *SANITIZE_HOST_FLAGS,
-          "-Xarch_host", "-fno-omit-frame-pointer", os.path.join(CSRC, "head_host.hip"), "-o", host], verbose)
-    others = [os.path.join(OBJDIR, f + ".o") for f in HEAD_SOURCES if f != "head_host.hip"]
-    missing = [o for o in others if not os.path.exists(o)]
-    if missing:
-        raise RuntimeError(f"build the library first; missing {missing}")
-    _link([host, *others], SANITIZED_HEAD_LIB, [*SANITIZE_HOST_FLAGS, "-shared-libsan"], verbose)
-    return SANITIZED_HEAD_LIB
+    return _build_sanitized("head_host.hip", HEAD_SOURCES, SANITIZED_HEAD_LIB, verbose)
+
+
+def build_sanitized_attn(verbose: bool = False) -> str:
+    """The same for the library between the projections (attn_host.hip); load it
+    with LITTLEBIT_ATTN_LIBRARY=<path>."""
+    return _build_sanitized("attn_host.hip", ATTN_SOURCES, SANITIZED_ATTN_LIB, verbose)
 
 
 STAMPED_LIB = os.path.join(LIBDIR, "stamped", "liblittlebit.so")
@@ -167,6 +185,7 @@ def build_library(verbose: bool = False, extra_flags=()) -> str:
     _link([objs[f] for f in LAYER_SOURCES], LIB, [], verbose)
     _link([objs[f] for f in INIT_SOURCES], INIT_LIB, ["-lrocblas", "-lrocsolver"], verbose)
     _link([objs[f] for f in HEAD_SOURCES], HEAD_LIB, [], verbose)
+    _link([objs[f] for f in ATTN_SOURCES], ATTN_LIB, [], verbose)
     return LIB
 
 
