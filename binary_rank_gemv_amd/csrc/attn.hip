@@ -25,6 +25,7 @@ namespace {
 typedef f16 h8 __attribute__((ext_vector_type(8)));
 typedef bf16 b8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLn2 = 0.693147180559945309f;
@@ -44,6 +45,10 @@ __device__ __forceinline__ u32x2 read_transposed(const uint8_t* lds) {
   const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lds);
   return __builtin_bit_cast(u32x2, v);
 }
+
+// Queries with the scale's sign, or 0 where it is 0: the scale that is left is positive, so that the largest score
+// is found before it is scaled, and -infinity stays what it is.
+__device__ __forceinline__ u32x4 with_sign(const LbAttnArgs& A, u32x4 q) { return (q ^ A.sign) & A.keep; }
 
 // Whether a word of two elements has a NaN or an infinity, and the word without them.
 template <typename T>
@@ -67,62 +72,57 @@ struct Place {
   int parts;      // parts of its keys
   int span;       // keys a part
   int local;      // of the sequence's blocks x parts
-  long slot;      // of its results, where there are several parts
+  int slot;       // of its results, where there are several parts
 };
 
-// Wave sums over 64 lanes of what each lane has, and what the lanes before it have.
+// What the lanes before this one have together, and all of them.
 __device__ __forceinline__ int scan64(int v, int* total) {
-  const int lane = threadIdx.x & 63;
   int s = v;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(s, d);
-    s += lane >= d ? o : 0;
-  }
+  s += __builtin_amdgcn_update_dpp(0, s, 0x111, 0xF, 0xF, false);  // one to the right in a row of 16, two, four, eight
+  s += __builtin_amdgcn_update_dpp(0, s, 0x112, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x114, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x118, 0xF, 0xF, false);
+  s += __builtin_amdgcn_update_dpp(0, s, 0x142, 0xA, 0xF, false);  // a row's last to the next row
+  s += __builtin_amdgcn_update_dpp(0, s, 0x143, 0xC, 0xF, false);  // the lower half's last to the upper half
   *total = __builtin_amdgcn_readlane(s, 63);
   return s - v;
 }
 
-struct Share {
-  int span, blocks, parts;
-  Span s;
-};
 __device__ __forceinline__ int blocks_of(const Span& s, int group, int rows) { return (s.rows * group + rows - 1) / rows; }
 __device__ __forceinline__ int parts_of(int keys, int span) { return max(1, (keys + span - 1) / span); }
 
-// The keys a part has.  The sum is in floating point, in one order everywhere: every
-// workgroup of the call, and the join, gets the same.
+// The place of item `item`.  A part has the keys, in steps of STEP, that spread all sequences' keys (times their
+// blocks of rows) over `target` workgroups.  Up to 64 sequences are read once.
 template <int STEP>
-__device__ __forceinline__ int span_for(const LbAttnArgs& A, int rows) {
+__device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int item) {
   const int lane = threadIdx.x & 63;
-  float units = 0.0f;
-  for (int i = lane; i < A.pages.seqs; i += 64) {
-    const Span s = span_of(A.pages, i, (int)A.tokens);
+  const int seqs = A.pages.seqs;
+  auto read = [&](int from) __attribute__((always_inline)) {
+    Span s = span_of(A.pages, min(from + lane, seqs - 1), (int)A.tokens);
+    if (from + lane >= seqs) s.rows = 0;
+    return s;
+  };
+  const Span first = read(0);
+  // in floating point, in one order everywhere: all workgroups get the same
+  float units = (float)first.keys * (float)blocks_of(first, A.group, rows);
+  for (int from = 64; from < seqs; from += 64) {
+    const Span s = read(from);
     units += (float)s.keys * (float)blocks_of(s, A.group, rows);
   }
   units = wave_sum(units) * (float)A.kv_heads / (float)A.target;
   const int want = max(kMinSpan, units < 1e9f ? (int)units + 1 : 1 << 30);
-  return __builtin_amdgcn_readfirstlane((want + STEP - 1) / STEP * STEP);
-}
-
-// The place of item `item` (BY_ROW false), or of the sequence `item` (BY_ROW true: local is 0).
-template <int STEP, bool BY_ROW>
-__device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int item) {
-  const int lane = threadIdx.x & 63;
   Place p;
   p.seq = -1;
-  p.span = span_for<STEP>(A, rows);
+  p.span = __builtin_amdgcn_readfirstlane((want + STEP - 1) / STEP * STEP);
   int items = 0, slots = 0;
-  for (int from = 0; from < A.pages.seqs; from += 64) {
-    const int i = from + lane;
-    const Span s = span_of(A.pages, min(i, A.pages.seqs - 1), (int)A.tokens);
-    const int blocks = i < A.pages.seqs ? blocks_of(s, A.group, rows) : 0;
+  for (int from = 0; from < seqs; from += 64) {
+    const Span s = from ? read(from) : first;
+    const int blocks = blocks_of(s, A.group, rows);
     const int parts = parts_of(s.keys, p.span);
     int all, all_slots;
     const int before = items + scan64(blocks * parts, &all);
     const int slots_before = slots + scan64(parts > 1 ? blocks * parts : 0, &all_slots);
-    const bool mine = BY_ROW ? i == item : blocks > 0 && item >= before && item < before + blocks * parts;
-    const uint64_t b = __ballot(mine);
+    const uint64_t b = __ballot(item >= before && item < before + blocks * parts);
     if (b) {
       const int l = __builtin_ctzll(b);
       p.seq = from + l;
@@ -132,7 +132,7 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
       p.s.base = __builtin_amdgcn_readlane(s.base, l);
       p.blocks = __builtin_amdgcn_readlane(blocks, l);
       p.parts = __builtin_amdgcn_readlane(parts, l);
-      p.local = BY_ROW ? 0 : item - __builtin_amdgcn_readlane(before, l);
+      p.local = item - __builtin_amdgcn_readlane(before, l);
       p.slot = __builtin_amdgcn_readlane(slots_before, l) + p.local;
       return p;
     }
@@ -148,7 +148,7 @@ struct Sight {
   int most, full;
 };
 __device__ __forceinline__ Sight sight_of(const LbAttnArgs& A, const Span& s, int first_row, int rows) {
-  const int last = min(first_row + rows, s.rows * A.group) - 1;
+  const int last = max(min(first_row + rows, s.rows * A.group), 1) - 1;
   Sight v;
   if (A.tree) {
     v.most = s.keys;
@@ -162,20 +162,65 @@ __device__ __forceinline__ Sight sight_of(const LbAttnArgs& A, const Span& s, in
   return v;
 }
 
-// Four channels of a row's result: scaled by the sum, or, of a part, as they are.
+// Four channels of a row's result, scaled by the sum.
 template <typename T>
-__device__ __forceinline__ void store_result(const LbAttnArgs& A, const Span& s, int kv_head, int row, int d, f32x4 o,
-                                             float m, float l) {
-  const int t = row / A.group, h = kv_head * A.group + row - t * A.group;
+__device__ __forceinline__ void store_result(const LbAttnArgs& A, int token, int head, int d, f32x4 o, float m, float l) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   if (d < A.dim) {
-    T* out = (T*)A.out + (s.start + t) * A.ot + h * A.oh + d;
+    T* out = (T*)A.out + token * A.ot + head * A.oh + d;
     u32x2 w;
     w[0] = Pair<T>::pack(l == 0.0f ? 0.0f : o[0] * inv, l == 0.0f ? 0.0f : o[1] * inv);
     w[1] = Pair<T>::pack(l == 0.0f ? 0.0f : o[2] * inv, l == 0.0f ? 0.0f : o[3] * inv);
     store_any(out, w);
   }
-  if (d == 0 && A.lse) A.lse[(long)(s.start + t) * A.heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (d == 0 && A.lse) A.lse[(long)token * A.heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// Where the parts of a row's result lie: part j in row first + j * step of the workspace.
+// One for each row of the call, written by its first part.
+struct Parts {
+  int first, count;
+};
+struct Workspace {
+  float* sums;    // [slots][kv_heads][rows][dim]
+  float2* ml;     // [slots][kv_heads][rows]: maximum, sum
+  Parts* parts;   // [tokens][heads]
+};
+__device__ __forceinline__ Workspace workspace_of(const LbAttnArgs& A, int rows) {
+  const long all = A.slots * A.kv_heads * rows;
+  Workspace w;
+  w.sums = A.partial;
+  w.ml = (float2*)(A.partial + all * A.dim);
+  w.parts = (Parts*)(w.ml + all);
+  return w;
+}
+
+// Four channels of row `row` of a sequence (row `in_block` of its block): the result itself, or of one of several parts.
+template <typename T>
+__device__ __forceinline__ void store_part(const LbAttnArgs& A, const Place& p, int kv_head, int rows, int part, int parts,
+                                           int row, int in_block, int d, f32x4 o, float m, float l) {
+  const int t = row / A.group, token = p.s.start + t, head = kv_head * A.group + row - t * A.group;
+  if (parts == 1) {
+    store_result<T>(A, token, head, d, o, m, l);
+  }
+  if (parts > 1 || d == 0) {
+    const Workspace w = workspace_of(A, rows);
+    const int at = (p.slot * A.kv_heads + kv_head) * rows + in_block;
+    if (parts > 1 && d < A.dim) *(f32x4*)(w.sums + (long)at * A.dim + d) = o;
+    if (d == 0) {
+      if (parts > 1) w.ml[at] = float2{m, l};
+      if (part == 0) w.parts[(long)token * A.heads + head] = Parts{at, parts};
+    }
+  }
+}
+
+// A stage holds rows of DP channels.  16-byte piece c of row r lies at place c ^ swizzle(r): the 16 rows of a
+// read fall on all banks, and so do the four rows of a transposing read, whose pieces are two or four in
+// a row: the row's last bits move them by fours.
+template <int DP>
+__device__ __forceinline__ int swizzle(int row) {
+  if constexpr (DP == 64) return (row & 2) << 1 | (row >> 2 & 3);  // two rows of 128 bytes fill the banks
+  return (row & 3) << 2 | (row >> 2 & 3);
 }
 
 // ------------------------------------------------------------------------ few rows
@@ -184,13 +229,6 @@ __device__ __forceinline__ void store_result(const LbAttnArgs& A, const Span& s,
 // from the products with this one's on, its values from their products on.  No wave waits for another until the
 // end, when the waves' sums are joined in LDS.  Bytes bound it.
 //
-// A stage holds 32 rows of DP channels.  16-byte piece c of row r lies at place c ^ swizzle(r), so that
-// the 16 rows of a read, and the transposing read's 16 rows x 32 bytes, fall on all banks.
-template <int DP>
-__device__ __forceinline__ int swizzle(int row) {
-  return DP == 64 ? (row >> 1) & 7 : row & 15;
-}
-
 template <typename T, int DP, int NT, int W>
 __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs A) {
   constexpr int kRowBytes = 2 * DP, kPieces = DP / 8, kStage = 32 * kRowBytes;
@@ -203,7 +241,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
   const int w = wave_id(), lane = threadIdx.x & 63;
   const int r16 = lane & 15, g = lane >> 4;
   const int kv_head = blockIdx.x % A.kv_heads;
-  const Place p = place_of<32 * W, false>(A, kRows, blockIdx.x / A.kv_heads);
+  const Place p = place_of<32 * W>(A, kRows, blockIdx.x / A.kv_heads);
   if (p.seq < 0) return;  // the whole workgroup: all waves computed the same
   // causal rows: the last block, which sees the most, first
   const int block = p.blocks - 1 - p.local / p.parts, part = p.local % p.parts;
@@ -240,7 +278,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
 #pragma unroll
     for (int s = 0; s < DP / 32; ++s) {
       const int d = 32 * s + 8 * g;
-      q[n][s] = in && d < A.dim ? load_any<u32x4>(src + d) : u32x4{0, 0, 0, 0};
+      q[n][s] = in && d < A.dim ? with_sign(A, load_any<u32x4>(src + d)) : u32x4{0, 0, 0, 0};
     }
     word[n] = A.tree && in ? (uint64_t)A.tree[p.s.start + t] : 0;
     sees[n] = in ? A.tree ? sight.most : min(sight.most, p.s.base + t + 1) : 0;
@@ -373,7 +411,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
       for (int n = 0; n < NT; ++n) {
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = st[n][i >> 2][i & 3] * A.scale;
+        for (int i = 0; i < 8; ++i) x[i] = st[n][i >> 2][i & 3];
         if (masked) {
           const uint32_t v = seen(n, key, here.good) >> (4 * g);
 #pragma unroll
@@ -384,7 +422,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
 #pragma unroll
         for (int i = 1; i < 8; ++i) most = fmaxf(most, x[i]);
         most = fmaxf(most, lane_xor<16>(most));
-        most = fmaxf(most, lane_xor<32>(most));
+        most = fmaxf(most, lane_xor<32>(most)) * A.scale;
         if (__ballot(most > m[n] + kSlack)) {
           const float up = fmaxf(m[n], most);
           const float a = m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[n] - up);
@@ -396,7 +434,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
         const float at = m[n] == -INFINITY ? 0.0f : m[n];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[i] = __builtin_amdgcn_exp2f(x[i] - at);
+          x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], A.scale, -at));
           l[n] += x[i];
         }
 #pragma unroll
@@ -485,61 +523,473 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
         total += v.x == -INFINITY ? v.y : a * v.y;
         sum += a * join[(j * 16 + r) * (DP / 4) + (c ^ r)];
       }
-      if (parts == 1) {
-        store_result<T>(A, p.s, kv_head, row, 4 * c, sum, top, total);
-      } else if (4 * c < A.dim) {
-        const long at = (p.slot * A.kv_heads + kv_head) * kRows + row - first_row;
-        *(f32x4*)(A.partial + at * A.dim + 4 * c) = sum;
-        if (c == 0) ((float2*)(A.partial + A.slots * A.kv_heads * kRows * A.dim))[at] = float2{top, total};
+      store_part<T>(A, p, kv_head, kRows, part, parts, row, row - first_row, 4 * c, sum, top, total);
+    }
+  }
+}
+
+// ----------------------------------------------------------------------- many rows
+// A workgroup of four waves has 128 RT rows of a sequence and key head, each wave 32 RT of them as the columns of 32 x 32
+// matrix steps, and all its keys in tiles of KT x 32, which the waves load into LDS together and all read.  The products
+// bound it, and the exponentials beside them: a wave's instructions are laid out so that the two run side by side.
+// While step j's scores become probabilities, the products of step j + 1's keys are formed; while the maxima of
+// step j + 1 are taken, those of step j's values.  Every operand that is read from LDS serves RT products.
+//
+// Keys have two stages, values three: a tile's values are read until one step after its keys.  One barrier a tile,
+// where the next tile has landed; the one after it is then asked for.
+template <typename T>
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (__is_same(T, f16))
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+}
+
+// 16 bytes a lane from base + offset to LDS, 1 KB from `lds` on.  In assembly, so that the compiler does not wait for it
+// before reads of other stages; the kernel waits itself.  Nothing is loaded into registers.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* base, uint32_t offset) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
+}
+
+template <typename T, int DP, int RT, int KT, int W>
+__global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A) {
+  constexpr int kRowBytes = 2 * DP, kPieces = DP / 8, kKeys = 32 * KT, kStage = kKeys * kRowBytes;
+  constexpr int kPer = 1024 / kRowBytes;       // keys of one load of a wave
+  constexpr int kLoads = kStage / 1024 / W;    // loads of a wave for a tile's keys, and for its values
+  constexpr int kRows = 32 * RT * W, kS = DP / 16, kD = DP / 32;
+  static_assert(kPer <= 8 && kLoads * 1024 * W == kStage, "a load lies in one page");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[5 * kStage];
+  const int w = wave_id(), lane = threadIdx.x & 63;
+  const int r32 = lane & 31, h = lane >> 5;
+  const int kv_head = blockIdx.x % A.kv_heads;
+  const Place p = place_of<kKeys>(A, kRows, blockIdx.x / A.kv_heads);
+  if (p.seq < 0) return;  // the whole workgroup: all waves computed the same
+  // causal rows: the last block, which sees the most, first
+  const int block = p.blocks - 1 - p.local / p.parts, part = p.local % p.parts;
+  const int all_rows = p.s.rows * A.group;
+  const Sight sight = sight_of(A, p.s, block * kRows, kRows);
+  const int parts = parts_of(sight.most, p.span);
+  if (part >= parts) return;
+  const int from = part * p.span, to = min(from + p.span, sight.most);
+  const int first_row = block * kRows + 32 * RT * w;
+  // this wave's own rows: their keys end earlier, and may be seen by all of them later
+  const bool has_rows = first_row < all_rows;
+  const Sight own = sight_of(A, p.s, first_row, 32 * RT);
+  const int steps = has_rows ? (max(min(own.most, to) - from, 0) + 31) / 32 : 0;
+  const int tiles = (max(to - from, 0) + kKeys - 1) / kKeys;
+
+  const LbPages& P = A.pages;
+  const char* const k_head = P.k + kv_head * P.head;
+  const char* const v_head = P.v + kv_head * P.head;
+  uint8_t* const k_lds = lds;
+  uint8_t* const v_lds = lds + 2 * kStage;
+  const bool padded = A.dim < DP;
+  if (padded) {  // pieces that no load fills
+    for (int i = threadIdx.x; i < 5 * kStage / 16; i += 64 * W) *(u32x4*)(lds + 16 * i) = u32x4{0, 0, 0, 0};
+    __syncthreads();
+  }
+
+  // queries, operands of S^T = K Q^T: row r32 of a tile, channels 16 s + 8 h + (0..7)
+  u32x4 q[RT][kS];
+  int sees[RT];
+  uint64_t word[RT];
+#pragma unroll
+  for (int n = 0; n < RT; ++n) {
+    const int row = first_row + 32 * n + r32;
+    const bool in = row < all_rows;
+    const int t = in ? row / A.group : 0, head = kv_head * A.group + (in ? row - t * A.group : 0);
+    const T* src = (const T*)A.q + (p.s.start + t) * A.qt + head * A.qh;
+#pragma unroll
+    for (int s = 0; s < kS; ++s) {
+      const int d = 16 * s + 8 * h;
+      q[n][s] = in && d < A.dim ? with_sign(A, load_any<u32x4>(src + d)) : u32x4{0, 0, 0, 0};
+    }
+    word[n] = A.tree && in ? (uint64_t)A.tree[p.s.start + t] : 0;
+    sees[n] = in ? A.tree ? sight.most : min(sight.most, p.s.base + t + 1) : 0;
+  }
+
+  typedef const __attribute__((address_space(4))) int32_t* Table;
+  const Table table = (Table)(uintptr_t)(P.table + p.seq * P.table_stride);
+  const int mask = (1 << P.shift) - 1;
+  auto page_at = [&](int key) __attribute__((always_inline)) { return table[min(key >> P.shift, P.columns - 1)]; };
+  auto is_page = [&](int page) __attribute__((always_inline)) { return (uint32_t)page < (uint32_t)P.pages; };
+  // this wave's part of tile t's keys and values into their stages
+  const int load_row = lane / kPieces, load_piece = lane % kPieces;
+  auto fill = [&](int t) __attribute__((always_inline)) {
+    const int key0 = from + t * kKeys;
+    uint8_t* const k_to = k_lds + (t & 1) * kStage;
+    uint8_t* const v_to = v_lds + (t % 3) * kStage;
+    int page[kLoads];
+    bool whole = key0 + kKeys <= sight.most;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      page[i] = page_at(key0 + kPer * (kLoads * w + i));
+      whole = whole && is_page(page[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = kPer * (kLoads * w + i), row = at + load_row, piece = load_piece ^ swizzle<DP>(row);
+      const long src = page[i] * P.page + ((key0 + at) & mask) * P.slot;
+      const uint32_t offset = load_row * (int)P.slot + 16 * piece;
+      if (whole) {
+        if (!padded || 8 * piece < A.dim) {
+          load_to_lds((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)k_to + at * kRowBytes, k_head + src, offset);
+          load_to_lds((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)v_to + at * kRowBytes, v_head + src, offset);
+        }
+      } else {
+        const bool in = key0 + row < sight.most && is_page(page[i]) && 8 * piece < A.dim;
+        u32x4 k = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+        if (in) {
+          k = *(const u32x4*)(k_head + src + offset);
+          v = *(const u32x4*)(v_head + src + offset);
+        }
+        *(u32x4*)(k_to + at * kRowBytes + 16 * lane) = k;
+        *(u32x4*)(v_to + at * kRowBytes + 16 * lane) = v;
       }
+    }
+  };
+  // the tile that was asked for has landed, in all waves, and every wave is past the stages that come next
+  auto meet = [&]() __attribute__((always_inline)) {
+    __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+  };
+
+  // which of a step's keys row n sees
+  auto below = [](int n) __attribute__((always_inline)) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+  auto seen = [&](int n, int key, uint32_t there) __attribute__((always_inline)) {
+    uint32_t v = below(sees[n] - key) & there;
+    if (A.tree) {
+      const int before = p.s.base - key;
+      const uint32_t drafted = before >= 32 ? 0u : before >= 0 ? (uint32_t)(word[n] << before)
+                               : before > -64 ? (uint32_t)(word[n] >> -before) : 0u;
+      v &= below(before) | drafted;
+    }
+    return v;
+  };
+  // keys of a step that have a page, a bit each
+  auto paged = [&](int key) __attribute__((always_inline)) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v |= is_page(page_at(key + 8 * i)) ? 0xFFu << (8 * i) : 0u;
+    return v;
+  };
+
+  f32x16 st[2][RT], o[RT][kD];
+  u32x4 pr[RT][2];
+  float m[RT], l[RT];
+  uint32_t there[2];
+#pragma unroll
+  for (int n = 0; n < RT; ++n) {
+    m[n] = -INFINITY;
+    l[n] = 0.0f;
+    pr[n][0] = pr[n][1] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < kD; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[n][d][i] = 0.0f;
+  }
+  const int k_at = r32 * kRowBytes + 16 * (h ^ swizzle<DP>(r32));
+  const int v_row = 4 * h + ((lane & 15) >> 2);
+  const int v_at = v_row * kRowBytes + 16 * ((2 * (lane >> 4 & 1) + ((lane & 3) >> 1)) ^ swizzle<DP>(v_row)) + 8 * (lane & 1);
+  // where step j's keys and values begin in LDS
+  auto k_of = [&](int j) __attribute__((always_inline)) { return (j / KT & 1) * kStage + j % KT * 32 * kRowBytes; };
+  auto v_of = [&](int j) __attribute__((always_inline)) { return (2 + j / KT % 3) * kStage + j % KT * 32 * kRowBytes; };
+
+  auto scores = [&](int j, f32x16 (&s)[RT]) __attribute__((always_inline)) {
+    const int at = k_of(j) + k_at;
+#pragma unroll
+    for (int n = 0; n < RT; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kS; ++c) {
+      const u32x4 k = *(const u32x4*)(lds + (at ^ (32 * c)));
+#pragma unroll
+      for (int n = 0; n < RT; ++n) s[n] = mfma32<T>(k, q[n][c], s[n]);
+    }
+  };
+  // what is not seen taken out
+  auto mask_scores = [&](int j, f32x16 (&s)[RT], uint32_t& t) __attribute__((always_inline)) {
+    const int key = from + 32 * j;
+    t = paged(key);
+    if (key + 32 > own.full || t != ~0u) {
+#pragma unroll
+      for (int n = 0; n < RT; ++n) {
+        const uint32_t v = seen(n, key, t) >> (4 * h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!(v >> (8 * (i >> 2) + (i & 3)) & 1)) s[n][i] = -INFINITY;
+      }
+    }
+  };
+  auto products = [&](int j) __attribute__((always_inline)) {
+    const int at = v_of(j) + v_at;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int d = 0; d < kD; ++d) {
+        const u32x2 v0 = read_transposed(lds + (at ^ (64 * d)) + 16 * s * kRowBytes);
+        const u32x2 v1 = read_transposed(lds + (at ^ (64 * d) ^ 32) + (16 * s + 8) * kRowBytes);
+        const u32x4 v = {v0[0], v0[1], v1[0], v1[1]};
+#pragma unroll
+        for (int n = 0; n < RT; ++n) o[n][d] = mfma32<T>(v, pr[n][s], o[n][d]);
+      }
+    }
+  };
+  // The same where a key that some rows do not see has a NaN or an infinity among its values: they are added to the
+  // rows that see it, and left out of the products.
+  auto odd_keys = [&](int j) __attribute__((always_inline)) {
+    uint32_t odd = 0;
+    const int at = v_of(j);
+#pragma unroll
+    for (int i = 0; i < 32 / kPer; ++i) {
+      const u32x4 v = *(const u32x4*)(lds + at + 1024 * i + 16 * lane);
+      const uint64_t b = __ballot(odd_word<T>(v[0]) || odd_word<T>(v[1]) || odd_word<T>(v[2]) || odd_word<T>(v[3]));
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (b >> (e * kPieces) & (1ull << kPieces) - 1) odd |= 1u << (kPer * i + e);
+    }
+    return odd;
+  };
+  auto odd_products = [&](int j, uint32_t odd, uint32_t t) __attribute__((always_inline)) {
+    const int at = v_of(j), key = from + 32 * j;
+    for (uint32_t left = odd; left; left &= left - 1) {
+      const int row = __builtin_ctz(left);
+#pragma unroll
+      for (int d = 0; d < kD; ++d) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const u32x2 v = *(const u32x2*)(lds + at + row * kRowBytes + 16 * ((4 * d + i) ^ swizzle<DP>(row)) + 8 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t e16 = v[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
+            if (!odd_word<T>(e16)) continue;
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+              if (seen(n, key, t) >> row & 1) o[n][d][4 * i + e] += Pair<T>::lo(e16);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int d = 0; d < kD; ++d) {
+        const u32x2 v0 = read_transposed(lds + ((at + v_at) ^ (64 * d)) + 16 * s * kRowBytes);
+        const u32x2 v1 = read_transposed(lds + ((at + v_at) ^ (64 * d) ^ 32) + (16 * s + 8) * kRowBytes);
+        const u32x4 v = {even_word<T>(v0[0]), even_word<T>(v0[1]), even_word<T>(v1[0]), even_word<T>(v1[1])};
+#pragma unroll
+        for (int n = 0; n < RT; ++n) o[n][d] = mfma32<T>(v, pr[n][s], o[n][d]);
+      }
+    }
+  };
+  // the largest score of each row so far
+  auto maxima = [&](const f32x16 (&s)[RT], float (&most)[RT]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < RT; ++n) {
+      float a = s[n][0], b = s[n][1];
+#pragma unroll
+      for (int i = 2; i < 16; i += 2) {
+        a = fmaxf(a, s[n][i]);
+        b = fmaxf(b, s[n][i + 1]);
+      }
+      a = fmaxf(a, b);
+      most[n] = fmaxf(a, lane_xor<32>(a)) * A.scale;
+    }
+  };
+  auto rescale = [&](const float (&most)[RT]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < RT; ++n) {
+      if (__ballot(most[n] > m[n] + kSlack)) {
+        const float up = fmaxf(m[n], most[n]);
+        const float a = m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[n] - up);
+        m[n] = up;
+        l[n] *= a;
+#pragma unroll
+        for (int d = 0; d < kD; ++d) o[n][d] *= a;
+      }
+    }
+  };
+  auto probabilities = [&](const f32x16 (&s)[RT]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < RT; ++n) {
+      const float at = m[n] == -INFINITY ? 0.0f : m[n];
+      float x[16];
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], A.scale, -at));
+        sum += x[i];
+      }
+      l[n] += sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pr[n][i >> 2][i & 3] = Pair<T>::pack(x[2 * i], x[2 * i + 1]);
+    }
+  };
+
+  if (tiles > 0) {
+    fill(0);
+    meet();
+    if (tiles > 1) fill(1);
+    float most[RT];
+    if (steps > 0) {
+      scores(0, st[0]);
+      mask_scores(0, st[0], there[0]);
+      maxima(st[0], most);
+      rescale(most);
+    }
+    auto body = [&](auto parity, int j) __attribute__((always_inline)) {
+      constexpr int B = decltype(parity)::value;
+      const int next = j + 1;
+      if (next % KT == 0 && next / KT < tiles) {
+        meet();
+        if (next / KT + 1 < tiles) fill(next / KT + 1);
+      }
+      if (j < steps) {
+        if (next < steps) {
+          scores(next, st[1 - B]);
+          probabilities(st[B]);
+          mask_scores(next, st[1 - B], there[1 - B]);
+        } else {
+          probabilities(st[B]);
+        }
+        const int key = from + 32 * j;
+        uint32_t odd = 0;
+        if (key + 32 > own.full) odd = odd_keys(j);
+        if (odd)
+          odd_products(j, odd, there[B]);
+        else
+          products(j);
+        if (next < steps) {
+          maxima(st[1 - B], most);
+          rescale(most);
+        }
+      }
+    };
+    for (int j = 0; j < tiles * KT; j += 2) {
+      body(std::integral_constant<int, 0>(), j);
+      if (j + 1 < tiles * KT) body(std::integral_constant<int, 1>(), j + 1);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < RT; ++n) {
+    l[n] += lane_xor<32>(l[n]);
+    const int row = first_row + 32 * n + r32;
+    if (row < all_rows) {
+#pragma unroll
+      for (int d = 0; d < kD; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f32x4 v = {o[n][d][4 * i], o[n][d][4 * i + 1], o[n][d][4 * i + 2], o[n][d][4 * i + 3]};
+          store_part<T>(A, p, kv_head, kRows, part, parts, row, row - block * kRows, 32 * d + 8 * i + 4 * h, v, m[n], l[n]);
+        }
     }
   }
 }
 
 // ------------------------------------------------------------------------- the join
-// A wave a token and key head; the parts' maxima and sums first, then four channels a lane.
-template <typename T, int STEP>
-__global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, int rows) {
+// Rows of the call whose keys were taken in parts.  A wave looks at `per` rows' records at once and joins those
+// with several parts, one after the other: all parts' maxima first, 64 at a time, then their sums, four channels a lane
+// and 64 / LD parts at a time.  A part in which a row saw nothing has no maximum, and a sum of 0 (or NaN).
+template <typename T, int LD>
+__global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, int rows, int per) {
+  constexpr int kSets = 64 / LD;
   const int w = wave_id(), lane = threadIdx.x & 63;
-  const long item = blockIdx.x * 4l + w;
-  const int token = (int)(item / A.kv_heads), kv_head = (int)(item - (long)token * A.kv_heads);
-  if (token >= A.tokens) return;
-  const int seq = sequence_of(A.pages, token);
-  if (seq < 0) return;
-  const Place p = place_of<STEP, true>(A, rows, seq);
-  const int t = token - p.s.start;
-  if (t >= p.s.rows) return;
-  const float2* const ml = (const float2*)(A.partial + A.slots * A.kv_heads * rows * A.dim);
-  for (int row = t * A.group; row < (t + 1) * A.group; ++row) {
-    const int block = row / rows;
-    const int parts = parts_of(sight_of(A, p.s, block * rows, rows).most, p.span);
-    if (parts == 1) continue;
-    const long slot = p.slot + (long)(p.blocks - 1 - block) * p.parts;
-    auto at = [&](int j) __attribute__((always_inline)) { return ((slot + j) * A.kv_heads + kv_head) * rows + row % rows; };
-    float top = -INFINITY, total = 0.0f;
-    for (int j = 0; j < parts; ++j) top = fmaxf(top, ml[at(j)].x);
+  const long all_rows = A.tokens * A.heads;
+  const long row0 = (blockIdx.x * 4l + w) * per;
+  if (row0 >= all_rows) return;
+  const Workspace ws = workspace_of(A, rows);
+  const int first_token = A.pages.starts[0], end_token = A.pages.starts[A.pages.seqs];
+  const long mine = row0 + lane;
+  Parts r = {0, 0};
+  if (lane < per && mine < all_rows) r = ws.parts[mine];
+  const long limit = A.slots * A.kv_heads * rows;
+  const int step = A.kv_heads * rows;
+  const long token = mine / A.heads;
+  // rows of no sequence have no record
+  bool several = lane < per && mine < all_rows && token >= first_token && token < end_token && r.count > 1;
+  several = several && r.first >= 0 && r.first + (r.count - 1l) * step < limit;
+  const int set = lane / LD, d = 4 * (lane % LD);
+  const bool in = d < A.dim;
+  for (uint64_t left = __ballot(several); left; left &= left - 1) {
+    const int l = __builtin_ctzll(left);
+    const int first = __builtin_amdgcn_readlane(r.first, l), count = __builtin_amdgcn_readlane(r.count, l);
+    float top = -INFINITY;
+    for (int j = 0; j < count; j += 64) top = fmaxf(top, lane + j < count ? ws.ml[first + (lane + j) * step].x : -INFINITY);
+    top = fmaxf(top, lane_xor<1>(top));
+    top = fmaxf(top, lane_xor<2>(top));
+    top = fmaxf(top, lane_xor<4>(top));
+    top = fmaxf(top, lane_xor<8>(top));
+    top = fmaxf(top, lane_xor<16>(top));
+    top = fmaxf(top, lane_xor<32>(top));
     f32x4 sum = {0, 0, 0, 0};
-    for (int j = 0; j < parts; ++j) {
-      const float2 v = ml[at(j)];
-      const float a = v.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(v.x - top);
-      total += v.x == -INFINITY ? v.y : a * v.y;
-      if (4 * lane < A.dim) sum += a * *(const f32x4*)(A.partial + at(j) * A.dim + 4 * lane);
+    float total = 0.0f;
+    // eight sets' loads at a time; behind the last part it again, with factor 0
+#pragma unroll 1
+    for (int j = 0; j < count; j += 8 * kSets) {
+      float2 v[8];
+      f32x4 o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = first + min(j + kSets * i + set, count - 1) * step;
+        v[i] = ws.ml[at];
+        o[i] = in ? *(const f32x4*)(ws.sums + (long)at * A.dim + d) : f32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool real = j + kSets * i + set < count;
+        const float a = v[i].x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(v[i].x - top);
+        if (real) {
+          total += v[i].x == -INFINITY ? v[i].y : a * v[i].y;
+          sum += a * o[i];
+        }
+      }
     }
-    store_result<T>(A, p.s, kv_head, row, 4 * lane, sum, top, total);
+    if constexpr (LD <= 16) {
+      total += lane_xor<16>(total);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += lane_xor<16>(sum[e]);
+    }
+    if constexpr (LD <= 32) {
+      total += lane_xor<32>(total);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] += lane_xor<32>(sum[e]);
+    }
+    if (set == 0) {
+      const long row = row0 + l;
+      const int t = (int)(row / A.heads);
+      store_result<T>(A, t, (int)(row - (long)t * A.heads), d, sum, top, total);
+    }
   }
+}
+
+template <typename T, int LD>
+void launch_join(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
+  // a row a wave while there are few, so that they are joined side by side
+  const long rows = a.tokens * a.heads;
+  const int per = rows <= 4096 ? 1 : rows <= 65536 ? 16 : 64;
+  hipLaunchKernelGGL((lb_attn_join_kernel<T, LD>), dim3((unsigned)((rows + 4 * per - 1) / (4 * per))), dim3(256), 0, stream, a,
+                     plan.rows, per);
 }
 
 template <typename T, int DP, int NT, int W>
 void launch_stream(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
   hipLaunchKernelGGL((lb_attn_stream_kernel<T, DP, NT, W>), dim3((unsigned)plan.grid), dim3(64 * W), 0, stream, a);
-  const long waves = a.tokens * a.kv_heads;
-  hipLaunchKernelGGL((lb_attn_join_kernel<T, 32 * W>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream, a,
-                     plan.rows);
+  launch_join<T, DP / 4>(a, plan, stream);
+}
+
+template <typename T, int DP, int RT, int KT, int W>
+void launch_tile(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
+  hipLaunchKernelGGL((lb_attn_tile_kernel<T, DP, RT, KT, W>), dim3((unsigned)plan.grid), dim3(64 * W), 0, stream, a);
+  launch_join<T, DP / 4>(a, plan, stream);
 }
 
 template <typename T, int DP, int W>
 void launch_rows(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
-  if (plan.rows == 16)
+  if (plan.rows > 64)
+    launch_tile<T, DP, 1, DP == 256 ? 1 : 2, DP == 256 ? 4 : 8>(a, plan, stream);
+  else if (plan.rows == 16)
     launch_stream<T, DP, 1, W>(a, plan, stream);
   else if (DP == 256 || plan.rows == 32)
     launch_stream<T, DP, 2, W>(a, plan, stream);
@@ -565,16 +1015,16 @@ void launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream
 LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int heads, int kv_heads, int dim) {
   LbAttnPlan p;
   const int64_t group = heads / kv_heads, mean = (tokens * group + seqs - 1) / seqs;
-  p.rows = mean <= 16 ? 16 : mean <= 32 || dim > 128 ? 32 : 64;
-  p.target = 1024;
+  p.rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 && dim <= 128 ? 64 : dim <= 128 ? 256 : 128;
+  p.target = p.rows <= 64 ? 1024 : 512;
   const int64_t share = (p.target + kv_heads - 1) / kv_heads;
   p.slots = 2 * share + 8;
   p.grid = (share + tokens * group / p.rows + seqs + 8) * kv_heads;
   return p;
 }
 
-size_t lb_attn_workspace(const LbAttnPlan& plan, int kv_heads, int dim) {
-  return (size_t)plan.slots * kv_heads * plan.rows * (dim + 2) * sizeof(float);
+size_t lb_attn_workspace(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim) {
+  return (size_t)plan.slots * kv_heads * plan.rows * (dim + 2) * sizeof(float) + (size_t)tokens * heads * 2 * sizeof(int);
 }
 
 hipError_t lb_launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, int dtype, hipStream_t stream) {

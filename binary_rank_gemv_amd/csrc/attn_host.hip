@@ -316,7 +316,8 @@ size_t littlebit_cache_attention_workspace_bytes(const lb_cache* cache, const lb
   if (!cache || !batch || tokens < 1 || tokens > kMaxTokens || cache->heads < 1 || cache->heads > kMaxHeads || heads < 1 ||
       heads > kMaxHeads || heads % cache->heads || batch->seqs < 1 || cache->dim < 2 || cache->dim > LB_HEAD_MAX_DIM)
     return 0;
-  return lb_attn_workspace(lb_attn_plan(tokens, batch->seqs, heads, cache->heads, cache->dim), cache->heads, cache->dim);
+  return lb_attn_workspace(lb_attn_plan(tokens, batch->seqs, heads, cache->heads, cache->dim), tokens, heads, cache->heads,
+                           cache->dim);
 }
 
 lb_status littlebit_cache_attention_fwd(const lb_cache* cache, const lb_cache_batch* batch, int64_t tokens,
@@ -329,15 +330,15 @@ lb_status littlebit_cache_attention_fwd(const lb_cache* cache, const lb_cache_ba
   LB_TRY(check_pair(name, "q", q, "out", out, tokens, cache->dim));
   if (q->heads % cache->heads)
     return fail(LB_ERR_INVALID_ARG, "%s: %d heads are no multiple of the cache's %d", name, q->heads, cache->heads);
-  if (!isfinite(scale)) return fail(LB_ERR_INVALID_ARG, "%s: scale must be finite", name);
+  if (!(fabsf(scale) <= 1e30f)) return fail(LB_ERR_INVALID_ARG, "%s: scale must be finite, at most 1e30", name);
   if (!aligned(tree, 8)) return fail(LB_ERR_INVALID_ARG, "%s: tree must be 8-byte aligned", name);
   if (!aligned(lse, 4)) return fail(LB_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", name);
   if (tokens == 0) return LB_OK;
   if (q->p == out->p) return fail(LB_ERR_INVALID_ARG, "%s: out must not be q", name);
   const LbAttnPlan plan = lb_attn_plan(tokens, batch->seqs, q->heads, cache->heads, cache->dim);
-  if (plan.grid > kMaxGroups || tokens * cache->heads > 4 * kMaxGroups)
+  if (plan.grid > kMaxGroups || tokens * q->heads > 4 * kMaxGroups)
     return fail(LB_ERR_UNSUPPORTED, "%s: %lld tokens of %d heads are too many for one call", name, (long long)tokens, q->heads);
-  const size_t need = lb_attn_workspace(plan, cache->heads, cache->dim);
+  const size_t need = lb_attn_workspace(plan, tokens, q->heads, cache->heads, cache->dim);
   if (!ws || !aligned(ws, 16)) return fail(LB_ERR_WORKSPACE, "%s: workspace must be given, 16-byte aligned", name);
   if (ws_bytes < need) return fail(LB_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", name, ws_bytes, need);
   LbAttnArgs a = {};
@@ -353,7 +354,10 @@ lb_status littlebit_cache_attention_fwd(const lb_cache* cache, const lb_cache_ba
   a.kv_heads = cache->heads;
   a.group = q->heads / cache->heads;
   a.dim = cache->dim;
-  a.scale = (float)((double)scale * 1.4426950408889634074);
+  a.scale = (float)(fabs((double)scale) * 1.4426950408889634074);
+  a.sign = scale < 0.0f ? 0x80008000u : 0u;
+  a.keep = a.scale > 0.0f ? ~0u : 0u;
+  if (a.keep == 0) a.scale = 1.0f;
   a.target = plan.target;
   return done(lb_launch_attn(a, plan, cache->dtype, (hipStream_t)stream), name);
 }

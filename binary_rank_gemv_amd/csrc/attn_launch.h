@@ -63,11 +63,12 @@ struct LbAttnArgs {
   void* out; long ot, oh;
   const int64_t* tree;
   float* lse;
-  float* partial;          // [slots][rows of a block][dim], then (maximum, sum) of each row
+  float* partial;          // the workspace
   long slots;
   long tokens;
   int heads, kv_heads, group, dim;
-  float scale;             // with the factor to base 2
+  float scale;             // its size, with the factor to base 2; 1 where it is 0
+  uint32_t sign, keep;     // what of it goes into the queries' bits
   int target;              // workgroups that the keys are spread over
 };
 
@@ -84,5 +85,5 @@ hipError_t lb_launch_rope(LbRopeArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_rope_bwd(const LbRopeBwdArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_accept(const LbPages& p, int heads, int dim, const int32_t* path, int columns, hipStream_t stream);
 LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int heads, int kv_heads, int dim);
-size_t lb_attn_workspace(const LbAttnPlan& plan, int kv_heads, int dim);
+size_t lb_attn_workspace(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim);
 hipError_t lb_launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, int dtype, hipStream_t stream);

@@ -162,7 +162,7 @@ lb_status littlebit_cache_append(const lb_cache *cache, const lb_cache_batch *ba
  *              sequence has at most LB_TREE_MAX rows then; keys of later ones are not seen.
  * What a row does not see has no part in its output, NaN and infinities in it included.
  * A row that sees nothing has output 0 and lse -infinity.
- *   scale      finite.
+ *   scale      finite, 1e30 at most in size; may be negative or 0.
  *   out        as q; overlaps no input.
  *   lse        fp32 tokens x q->heads, or NULL: the logarithm of the sum of exp(scale q . k_j).
  *   ws         littlebit_cache_attention_workspace_bytes(...) bytes, 16-byte aligned.
