@@ -678,7 +678,6 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   f32x16 st[2][RT], o[RT][kD];
   u32x4 pr[RT][2];
   float m[RT], l[RT];
-  uint32_t there[2];
 #pragma unroll
   for (int n = 0; n < RT; ++n) {
     m[n] = -INFINITY;
@@ -707,20 +706,6 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
       const u32x4 k = *(const u32x4*)(lds + (at ^ (32 * c)));
 #pragma unroll
       for (int n = 0; n < RT; ++n) s[n] = mfma32<T>(k, q[n][c], s[n]);
-    }
-  };
-  // what is not seen taken out
-  auto mask_scores = [&](int j, f32x16 (&s)[RT], uint32_t& t) __attribute__((always_inline)) {
-    const int key = from + 32 * j;
-    t = paged(key);
-    if (key + 32 > own.full || t != ~0u) {
-#pragma unroll
-      for (int n = 0; n < RT; ++n) {
-        const uint32_t v = seen(n, key, t) >> (4 * h);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!(v >> (8 * (i >> 2) + (i & 3)) & 1)) s[n][i] = -INFINITY;
-      }
     }
   };
   auto products = [&](int j) __attribute__((always_inline)) {
@@ -815,62 +800,89 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
 #pragma unroll
     for (int n = 0; n < RT; ++n) {
       const float at = m[n] == -INFINITY ? 0.0f : m[n];
-      float x[16];
-      float sum = 0.0f;
+      float x[16], sum[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         x[i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], A.scale, -at));
-        sum += x[i];
+        sum[i & 1] += x[i];
       }
-      l[n] += sum;
+      l[n] += sum[0] + sum[1];
 #pragma unroll
       for (int i = 0; i < 8; ++i) pr[n][i >> 2][i & 3] = Pair<T>::pack(x[2 * i], x[2 * i + 1]);
+    }
+  };
+  // before step j is left: where the next one begins a tile, that has landed in all waves, and the one after it is asked for
+  auto advance = [&](int j) __attribute__((always_inline)) {
+    const int t = (j + 1) / KT;
+    if ((j + 1) % KT == 0 && t < tiles) {
+      meet();
+      if (t + 1 < tiles) fill(t + 1);
     }
   };
 
   if (tiles > 0) {
     fill(0);
+    // whether every key has a page: the loop below does not ask again
+    bool good = true;
+    for (int c = (from >> P.shift) + lane; c <= (to - 1) >> P.shift; c += 64) good = good && is_page(P.table[p.seq * P.table_stride + c]);
+    const int clear = __ballot(!good) ? 0 : min(steps, (min(own.full, to) - from) >> 5);  // steps that all rows see whole
     meet();
     if (tiles > 1) fill(1);
     float most[RT];
-    if (steps > 0) {
+    int j = 0;
+    if (clear > 0) {
       scores(0, st[0]);
-      mask_scores(0, st[0], there[0]);
       maxima(st[0], most);
       rescale(most);
-    }
-    auto body = [&](auto parity, int j) __attribute__((always_inline)) {
-      constexpr int B = decltype(parity)::value;
-      const int next = j + 1;
-      if (next % KT == 0 && next / KT < tiles) {
-        meet();
-        if (next / KT + 1 < tiles) fill(next / KT + 1);
+      auto body = [&](auto parity, int j) __attribute__((always_inline)) {
+        constexpr int B = decltype(parity)::value;
+        advance(j);
+        scores(j + 1, st[1 - B]);
+        probabilities(st[B]);
+        products(j);
+        maxima(st[1 - B], most);
+        rescale(most);
+      };
+      // no way round a step's products in here: the outputs stay where they are
+      for (; j + 2 < clear; j += 2) {
+        body(std::integral_constant<int, 0>(), j);
+        body(std::integral_constant<int, 1>(), j + 1);
       }
-      if (j < steps) {
-        if (next < steps) {
-          scores(next, st[1 - B]);
-          probabilities(st[B]);
-          mask_scores(next, st[1 - B], there[1 - B]);
-        } else {
-          probabilities(st[B]);
-        }
-        const int key = from + 32 * j;
-        uint32_t odd = 0;
-        if (key + 32 > own.full) odd = odd_keys(j);
-        if (odd)
-          odd_products(j, odd, there[B]);
-        else
-          products(j);
-        if (next < steps) {
-          maxima(st[1 - B], most);
-          rescale(most);
-        }
+      if (j + 1 < clear) {
+        body(std::integral_constant<int, 0>(), j);
+        ++j;
+#pragma unroll
+        for (int n = 0; n < RT; ++n) st[0][n] = st[1][n];
       }
-    };
-    for (int j = 0; j < tiles * KT; j += 2) {
-      body(std::integral_constant<int, 0>(), j);
-      if (j + 1 < tiles * KT) body(std::integral_constant<int, 1>(), j + 1);
+      advance(j);
+      probabilities(st[0]);
+      products(j);
+      ++j;
     }
+    // the last keys, which not all rows see (all of them, where a page is missing), one step after the other
+#pragma unroll 1
+    for (; j < steps; ++j) {
+      const int key = from + 32 * j;
+      const uint32_t there = paged(key);
+      scores(j, st[0]);
+#pragma unroll
+      for (int n = 0; n < RT; ++n) {
+        const uint32_t v = seen(n, key, there) >> (4 * h);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!(v >> (8 * (i >> 2) + (i & 3)) & 1)) st[0][n][i] = -INFINITY;
+      }
+      maxima(st[0], most);
+      rescale(most);
+      probabilities(st[0]);
+      const uint32_t odd = odd_keys(j);
+      if (odd)
+        odd_products(j, odd, there);
+      else
+        products(j);
+      advance(j);
+    }
+    for (; j < tiles * KT; ++j) advance(j);
   }
 #pragma unroll
   for (int n = 0; n < RT; ++n) {
