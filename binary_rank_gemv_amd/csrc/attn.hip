@@ -29,7 +29,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr int kMinSpan = 256;   // keys a workgroup takes at least, where a sequence has them
 constexpr float kSlack = 8.0f;  // log2: how far a maximum may grow before the sums are scaled down
 
 template <typename T>
@@ -92,7 +91,9 @@ __device__ __forceinline__ int blocks_of(const Span& s, int group, int rows) { r
 __device__ __forceinline__ int parts_of(int keys, int span) { return max(1, (keys + span - 1) / span); }
 
 // The place of item `item`.  A part has the keys, in steps of STEP, that spread all sequences' keys (times their
-// blocks of rows) over `target` workgroups.  Up to 64 sequences are read once.
+// blocks of rows) over the workgroups that run at once, `round` of them, and no fewer than `least`.  Parts are rounded
+// up, at most one for each block, so that `round` less the blocks is what is shared out; where blocks are many, over
+// several rounds, so that the last parts are short beside the whole.  Up to 64 sequences are read once.
 template <int STEP>
 __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int item) {
   const int lane = threadIdx.x & 63;
@@ -104,13 +105,19 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
   };
   const Span first = read(0);
   // in floating point, in one order everywhere: all workgroups get the same
-  float units = (float)first.keys * (float)blocks_of(first, A.group, rows);
+  float blocks_all = (float)blocks_of(first, A.group, rows);
+  float units = (float)first.keys * blocks_all;
   for (int from = 64; from < seqs; from += 64) {
     const Span s = read(from);
-    units += (float)s.keys * (float)blocks_of(s, A.group, rows);
+    const float blocks = (float)blocks_of(s, A.group, rows);
+    blocks_all += blocks;
+    units += (float)s.keys * blocks;
   }
-  units = wave_sum(units) * (float)A.kv_heads / (float)A.target;
-  const int want = max(kMinSpan, units < 1e9f ? (int)units + 1 : 1 << 30);
+  blocks_all = wave_sum(blocks_all) * (float)A.kv_heads;
+  const float round = (float)A.round;
+  const float share = fminf(round * (1.0f + floorf(4.0f * blocks_all / round)) - blocks_all, (float)A.target);
+  units = wave_sum(units) * (float)A.kv_heads / fmaxf(share, round * 0.5f);
+  const int want = max(A.least, units < 1e9f ? (int)units + 1 : 1 << 30);
   Place p;
   p.seq = -1;
   p.span = __builtin_amdgcn_readfirstlane((want + STEP - 1) / STEP * STEP);
@@ -209,7 +216,7 @@ __device__ __forceinline__ void store_part(const LbAttnArgs& A, const Place& p, 
     if (parts > 1 && d < A.dim) *(f32x4*)(w.sums + (long)at * A.dim + d) = o;
     if (d == 0) {
       if (parts > 1) w.ml[at] = float2{m, l};
-      if (part == 0) w.parts[(long)token * A.heads + head] = Parts{at, parts};
+      if (part == 0 && A.slots > 0) w.parts[(long)token * A.heads + head] = Parts{at, parts};
     }
   }
 }
@@ -978,9 +985,10 @@ __global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, i
 
 template <typename T, int LD>
 void launch_join(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
+  if (!plan.join) return;
   // a row a wave while there are few, so that they are joined side by side
   const long rows = a.tokens * a.heads;
-  const int per = rows <= 4096 ? 1 : rows <= 65536 ? 16 : 64;
+  const int per = rows <= 8192 ? 1 : rows <= 65536 ? 4 : 64;
   hipLaunchKernelGGL((lb_attn_join_kernel<T, LD>), dim3((unsigned)((rows + 4 * per - 1) / (4 * per))), dim3(256), 0, stream, a,
                      plan.rows, per);
 }
@@ -1022,20 +1030,25 @@ void launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream
 }  // namespace
 
 // Rows of a workgroup by the rows that a sequence has on average.  A sequence of n rows has at most
-// n group / rows + 1 blocks, and `target` / kv_heads parts are added over all of them; a
-// sequence with several parts has at most twice its share of them.
-LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int heads, int kv_heads, int dim) {
+// n group / rows + 1 blocks, and `target` / kv_heads parts at most are added over all of them; sequences
+// with several parts have at most twice their share of them.
+LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int64_t capacity, int heads, int kv_heads, int dim) {
   LbAttnPlan p;
   const int64_t group = heads / kv_heads, mean = (tokens * group + seqs - 1) / seqs;
   p.rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 && dim <= 128 ? 64 : dim <= 128 ? 256 : 128;
-  p.target = p.rows <= 64 ? 1024 : 512;
+  // workgroups at once: by their LDS and registers
+  p.round = p.rows > 64 ? 256 : dim <= 64 && p.rows == 16 ? 1024 : 512;
+  p.target = p.rows > 64 ? 512 : p.rows == 16 ? 1536 : 1024;
+  p.least = p.rows > 64 ? 2048 : 256;
+  p.join = capacity > p.least;
   const int64_t share = (p.target + kv_heads - 1) / kv_heads;
-  p.slots = 2 * share + 8;
+  p.slots = p.join ? 2 * share + 8 : 0;
   p.grid = (share + tokens * group / p.rows + seqs + 8) * kv_heads;
   return p;
 }
 
 size_t lb_attn_workspace(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim) {
+  if (!plan.join) return 0;
   return (size_t)plan.slots * kv_heads * plan.rows * (dim + 2) * sizeof(float) + (size_t)tokens * heads * 2 * sizeof(int);
 }
 

@@ -314,9 +314,9 @@ lb_status littlebit_cache_append(const lb_cache* cache, const lb_cache_batch* ba
 size_t littlebit_cache_attention_workspace_bytes(const lb_cache* cache, const lb_cache_batch* batch, int64_t tokens,
                                                  int32_t heads) {
   if (!cache || !batch || tokens < 1 || tokens > kMaxTokens || cache->heads < 1 || cache->heads > kMaxHeads || heads < 1 ||
-      heads > kMaxHeads || heads % cache->heads || batch->seqs < 1 || cache->dim < 2 || cache->dim > LB_HEAD_MAX_DIM)
+      heads > kMaxHeads || heads % cache->heads || batch->seqs < 1 || batch->columns < 1 || cache->page_size < 1 || cache->dim < 2 || cache->dim > LB_HEAD_MAX_DIM)
     return 0;
-  return lb_attn_workspace(lb_attn_plan(tokens, batch->seqs, heads, cache->heads, cache->dim), tokens, heads, cache->heads,
+  return lb_attn_workspace(lb_attn_plan(tokens, batch->seqs, (int64_t)batch->columns * cache->page_size, heads, cache->heads, cache->dim), tokens, heads, cache->heads,
                            cache->dim);
 }
 
@@ -335,11 +335,12 @@ lb_status littlebit_cache_attention_fwd(const lb_cache* cache, const lb_cache_ba
   if (!aligned(lse, 4)) return fail(LB_ERR_INVALID_ARG, "%s: lse must be 4-byte aligned", name);
   if (tokens == 0) return LB_OK;
   if (q->p == out->p) return fail(LB_ERR_INVALID_ARG, "%s: out must not be q", name);
-  const LbAttnPlan plan = lb_attn_plan(tokens, batch->seqs, q->heads, cache->heads, cache->dim);
+  const LbAttnPlan plan = lb_attn_plan(tokens, batch->seqs, (int64_t)batch->columns * cache->page_size, q->heads, cache->heads, cache->dim);
   if (plan.grid > kMaxGroups || tokens * q->heads > 4 * kMaxGroups)
     return fail(LB_ERR_UNSUPPORTED, "%s: %lld tokens of %d heads are too many for one call", name, (long long)tokens, q->heads);
   const size_t need = lb_attn_workspace(plan, tokens, q->heads, cache->heads, cache->dim);
-  if (!ws || !aligned(ws, 16)) return fail(LB_ERR_WORKSPACE, "%s: workspace must be given, 16-byte aligned", name);
+  if (need > 0 && (!ws || !aligned(ws, 16)))
+    return fail(LB_ERR_WORKSPACE, "%s: workspace must be given, 16-byte aligned", name);
   if (ws_bytes < need) return fail(LB_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", name, ws_bytes, need);
   LbAttnArgs a = {};
   a.pages = pages_of(cache, batch);
@@ -358,7 +359,9 @@ lb_status littlebit_cache_attention_fwd(const lb_cache* cache, const lb_cache_ba
   a.sign = scale < 0.0f ? 0x80008000u : 0u;
   a.keep = a.scale > 0.0f ? ~0u : 0u;
   if (a.keep == 0) a.scale = 1.0f;
+  a.round = plan.round;
   a.target = plan.target;
+  a.least = plan.least;
   return done(lb_launch_attn(a, plan, cache->dtype, (hipStream_t)stream), name);
 }
 

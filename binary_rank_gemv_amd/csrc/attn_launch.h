@@ -69,13 +69,16 @@ struct LbAttnArgs {
   int heads, kv_heads, group, dim;
   float scale;             // its size, with the factor to base 2; 1 where it is 0
   uint32_t sign, keep;     // what of it goes into the queries' bits
-  int target;              // workgroups that the keys are spread over
+  int round, target, least;  // as in the plan
 };
 
 // The attention's shape for a call, a function of its sizes alone.
 struct LbAttnPlan {
   int rows;                // rows (tokens x heads of a group) of a workgroup
-  int target;
+  int round;               // workgroups that run at once
+  int target;              // and that the keys are spread over, at most
+  int least;               // keys of a part, at least
+  bool join;               // whether a sequence can have several parts
   long slots;              // workgroups whose results may have to be joined
   long grid;
 };
@@ -84,6 +87,6 @@ void lb_rope_bwd_groups(int64_t tokens, int heads, int kv_heads, int dim, int* g
 hipError_t lb_launch_rope(LbRopeArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_rope_bwd(const LbRopeBwdArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_accept(const LbPages& p, int heads, int dim, const int32_t* path, int columns, hipStream_t stream);
-LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int heads, int kv_heads, int dim);
+LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int64_t capacity, int heads, int kv_heads, int dim);
 size_t lb_attn_workspace(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim);
 hipError_t lb_launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, int dtype, hipStream_t stream);

@@ -165,7 +165,8 @@ lb_status littlebit_cache_append(const lb_cache *cache, const lb_cache_batch *ba
  *   scale      finite, 1e30 at most in size; may be negative or 0.
  *   out        as q; overlaps no input.
  *   lse        fp32 tokens x q->heads, or NULL: the logarithm of the sum of exp(scale q . k_j).
- *   ws         littlebit_cache_attention_workspace_bytes(...) bytes, 16-byte aligned.
+ *   ws         littlebit_cache_attention_workspace_bytes(...) bytes (may be 0, then ws may be
+ *              NULL), 16-byte aligned.
  * Scores, softmax and sums are in fp32; the probabilities are rounded to the cache's type for
  * their product with the values.  The same call gives the same bits.
  */

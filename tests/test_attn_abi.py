@@ -131,6 +131,9 @@ def test_append_refuses(kw, status):
     assert "littlebit_cache_append" in attn.littlebit_attn_last_error()
 
 
+LONG = B(columns=100, stride=100)   # more keys than one workgroup takes at least
+
+
 def _attend(c=C(), b=B(), tokens=3, q=H(), tree=None, scale=0.1, out=H(OUT), lse=None, ws=FAKE, nws=1 << 30):
     return attn.LIB.littlebit_cache_attention_fwd(r(c), r(b), tokens, r(q), tree, scale, r(out), lse, ws, nws, None)
 
@@ -138,7 +141,7 @@ def _attend(c=C(), b=B(), tokens=3, q=H(), tree=None, scale=0.1, out=H(OUT), lse
 @pytest.mark.parametrize("kw,status", CACHES + HEADS[:7] + [
     (dict(out=H(OUT, heads=2)), BAD), (dict(out=H()), BAD), (dict(out=None), BAD), (dict(q=H(heads=3), out=H(OUT, heads=3)), BAD),
     (dict(scale=float("nan")), BAD), (dict(tree=FAKE + 4), BAD), (dict(lse=FAKE + 2), BAD),
-    (dict(ws=None), WS), (dict(ws=FAKE + 8), WS), (dict(nws=100), WS), (dict(tokens=-1), BAD),
+    (dict(b=LONG, ws=None), WS), (dict(b=LONG, ws=FAKE + 8), WS), (dict(b=LONG, nws=100), WS), (dict(tokens=-1), BAD),
     (dict(c=C(heads=512, head=1024, page=512 * 1024), q=H(heads=1024, token=1 << 16), out=H(OUT, heads=1024, token=1 << 16), tokens=1 << 21), UNSUP),
 ])
 def test_attention_refuses(kw, status):
@@ -173,7 +176,8 @@ def test_workspace_sizes():
     assert 0 < W(1, 4, 4, 64) <= W(100, 4, 4, 64) and W(100, 0, 4, 64) > 0
     A = lambda c, b, t, h: attn.LIB.littlebit_cache_attention_workspace_bytes(r(c), r(b), t, h)  # noqa: E731
     assert A(C(), B(), 0, 4) == 0 and A(C(), B(), 3, 3) == 0 and A(None, B(), 3, 4) == 0 and A(C(), None, 3, 4) == 0
-    assert A(C(heads=0), B(), 3, 4) == 0 and A(C(), B(seqs=0), 3, 4) == 0 and A(C(), B(), 3, 4) > 0
+    assert A(C(heads=0), LONG, 3, 4) == 0 and A(C(), B(seqs=0), 3, 4) == 0 and A(C(), LONG, 3, 4) > 0
+    assert A(C(), B(), 3, 4) == 0   # short sequences: nothing to join
 
 
 def test_binding_refuses_what_is_not_on_a_gpu():
