@@ -45,6 +45,33 @@ __device__ __forceinline__ u32x2 read_transposed(const uint8_t* lds) {
   return __builtin_bit_cast(u32x2, v);
 }
 
+// The first n of 32 bits.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+
+// The keys of a step of 32, from `key` on, that a row sees, a bit each: of those that are there, those before `sees`,
+// and, of a tree, those before the rows' own and those of its word.
+__device__ __forceinline__ uint32_t seen_of(const LbAttnArgs& A, int base, int key, uint32_t there, int sees, uint64_t word) {
+  uint32_t v = below(sees - key) & there;
+  if (A.tree) {
+    const int before = base - key;
+    const uint32_t drafted = before >= 32 ? 0u : before >= 0 ? (uint32_t)(word << before)
+                             : before > -64 ? (uint32_t)(word >> -before) : 0u;
+    v &= below(before) | drafted;
+  }
+  return v;
+}
+
+// The larger of the sizes of two pairs of elements: of a NaN or an infinity, as bits, `kOdd` at least.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 size_max(u16x2 a, uint32_t w) {
+  return __builtin_elementwise_max(a, __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu));
+}
+template <typename T>
+__device__ __forceinline__ bool is_odd(u16x2 size) {
+  constexpr unsigned short odd = __is_same(T, f16) ? 0x7C00 : 0x7F80;
+  return size[0] >= odd || size[1] >= odd;
+}
+
 // Queries with the scale's sign, or 0 where it is 0: the scale that is left is positive, so that the largest score
 // is found before it is scaled, and -infinity stays what it is.
 __device__ __forceinline__ u32x4 with_sign(const LbAttnArgs& A, u32x4 q) { return (q ^ A.sign) & A.keep; }
@@ -206,7 +233,7 @@ __device__ __forceinline__ Workspace workspace_of(const LbAttnArgs& A, int rows)
 template <typename T>
 __device__ __forceinline__ void store_part(const LbAttnArgs& A, const Place& p, int kv_head, int rows, int part, int parts,
                                            int row, int in_block, int d, f32x4 o, float m, float l) {
-  const int t = row / A.group, token = p.s.start + t, head = kv_head * A.group + row - t * A.group;
+  const int t = (uint32_t)row / (uint32_t)A.group, token = p.s.start + t, head = kv_head * A.group + row - t * A.group;
   if (parts == 1) {
     store_result<T>(A, token, head, d, o, m, l);
   }
@@ -230,6 +257,56 @@ __device__ __forceinline__ int swizzle(int row) {
   return (row & 3) << 2 | (row >> 2 & 3);
 }
 
+// 16 bytes a lane from base + offset to LDS, 1 KB from `lds` on.  In assembly, so that the compiler does not wait for it
+// before reads of other stages; the kernels wait themselves.  Nothing is loaded into registers.
+__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* base, uint32_t offset) {
+  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
+                   "v"(offset), "s"(base)
+                   : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// Values of a key that some rows see and others do not may be NaN or infinite: their product with a 0 would be one
+// too.  Such values are cleared in the stage, and added at the end to the rows that see them (`odd` says that
+// there are any; the sums do not change by what was cleared, and nothing that is added to them is finite).
+// Clears those of the kLoads KB that this lane's wave has loaded.
+template <typename T, int LOADS>
+__device__ __forceinline__ bool clear_odd(uint8_t* stage) {
+  const int lane = threadIdx.x & 63;
+  u16x2 size = {0, 0};
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const u32x4 v = *(const u32x4*)(stage + 1024 * i + 16 * lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) size = size_max(size, v[e]);
+  }
+  if (__builtin_expect(__ballot(is_odd<T>(size)) == 0, 1)) return false;
+#pragma unroll 1
+  for (int i = 0; i < LOADS; ++i) {
+    u32x4 v = *(const u32x4*)(stage + 1024 * i + 16 * lane);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = even_word<T>(v[e]);
+    *(u32x4*)(stage + 1024 * i + 16 * lane) = v;
+  }
+  return true;
+}
+// The four values of channels d to d + 3 of a row at `p` that are odd, 0 in the place of the others.
+template <typename T>
+__device__ __forceinline__ f32x4 odd_values(const char* p, int d, int dim, bool there) {
+  f32x4 f = {0, 0, 0, 0};
+  if (there && d < dim) {
+    const u32x2 v = *(const u32x2*)(p + 2 * d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t w = v[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
+      f[e] = odd_word<T>(w) ? Pair<T>::lo(w) : 0.0f;
+    }
+  }
+  return f;
+}
+
 // ------------------------------------------------------------------------ few rows
 // 16 NT rows a workgroup; its W waves have the same rows and take turns at steps of 32 keys, each
 // with its own stages in LDS, filled by direct loads: the next step's keys are under way
@@ -237,7 +314,7 @@ __device__ __forceinline__ int swizzle(int row) {
 // end, when the waves' sums are joined in LDS.  Bytes bound it.
 //
 template <typename T, int DP, int NT, int W>
-__global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs A) {
+__global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream_kernel(const LbAttnArgs A) {
   constexpr int kRowBytes = 2 * DP, kPieces = DP / 8, kStage = 32 * kRowBytes;
   constexpr int kPer = 1024 / kRowBytes;   // keys of one load of the wave
   constexpr int kLoads = 32 / kPer;
@@ -263,6 +340,31 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
   const char* const v_head = P.v + kv_head * P.head;
   uint8_t* const ks = k_stages[w];
   uint8_t* const vs = v_stages[w];
+  const uint32_t k_lds = lds_address(ks), v_lds = lds_address(vs);
+  // pages of a step's keys, by eights (0 where there is none), and which of its keys are there
+  struct Pages {
+    int id[4];
+    uint32_t there;
+  };
+  const int mask = (1 << P.shift) - 1;
+  typedef const __attribute__((address_space(4))) int32_t* Table;  // read by the scalar unit: not counted with the loads
+  const Table table = (Table)(uintptr_t)(P.table + p.seq * P.table_stride);
+  auto lookup = [&](int key) __attribute__((always_inline)) {
+    Pages t;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t.id[i] = table[min((key + 8 * i) >> P.shift, P.columns - 1)];
+    t.there = below(sight.most - key);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((uint32_t)t.id[i] >= (uint32_t)P.pages) {
+        t.id[i] = 0;
+        t.there &= ~(0xFFu << (8 * i));
+      }
+    }
+    return t;
+  };
+  int key = from + 32 * w;
+  Pages here = lookup(key);
   const bool padded = A.dim < DP;
   if (padded) {  // pieces that no load fills
     for (int i = lane; i < kStage / 16; i += 64) {
@@ -280,7 +382,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
   for (int n = 0; n < NT; ++n) {
     const int row = first_row + 16 * n + r16;
     const bool in = row < all_rows;
-    const int t = in ? row / A.group : 0, h = kv_head * A.group + (in ? row - t * A.group : 0);
+    const int t = in ? (uint32_t)row / (uint32_t)A.group : 0, h = kv_head * A.group + (in ? row - t * A.group : 0);
     const T* src = (const T*)A.q + (p.s.start + t) * A.qt + h * A.qh;
 #pragma unroll
     for (int s = 0; s < DP / 32; ++s) {
@@ -290,69 +392,21 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
     word[n] = A.tree && in ? (uint64_t)A.tree[p.s.start + t] : 0;
     sees[n] = in ? A.tree ? sight.most : min(sight.most, p.s.base + t + 1) : 0;
   }
-  // the keys of a step of 32 that row n sees, a bit each
-  auto below = [](int n) __attribute__((always_inline)) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
-  auto seen = [&](int n, int key, int good) __attribute__((always_inline)) {
-    uint32_t v = below(sees[n] - key);
-    if (A.tree) {
-      const int before = p.s.base - key;  // keys of the step before the rows' own
-      const uint32_t drafted = before >= 32 ? 0u : before >= 0 ? (uint32_t)(word[n] << before)
-                               : before > -64 ? (uint32_t)(word[n] >> -before) : 0u;
-      v &= below(before) | drafted;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v &= good >> i & 1 ? ~0u : ~(0xFFu << (8 * i));
-    return v;
+  auto seen = [&](int n, int key, uint32_t there) __attribute__((always_inline)) {
+    return seen_of(A, p.s.base, key, there, sees[n], word[n]);
   };
 
-  // pages of a step's keys, by eights, and which of them are pages (a bit each)
-  struct Pages {
-    int id[4];
-    int good;
-  };
-  const int mask = (1 << P.shift) - 1;
-  typedef const __attribute__((address_space(4))) int32_t* Table;  // read by the scalar unit: not counted with the loads
-  const Table table = (Table)(uintptr_t)(P.table + p.seq * P.table_stride);
-  auto lookup = [&](int key) __attribute__((always_inline)) {
-    Pages t;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t.id[i] = table[min((key + 8 * i) >> P.shift, P.columns - 1)];
-    t.good = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) t.good |= ((uint32_t)t.id[i] < (uint32_t)P.pages ? 1 : 0) << i;
-    return t;
-  };
+  // a step of keys or values into its stage.  Memory that holds no key of the sequence is read too, but no other
+  // than the cache's: what is masked, or cleared, afterwards.
   const int load_row = lane / kPieces, load_piece = lane % kPieces;
   const int lane_at = load_row * (int)P.slot;
-  // a step of keys or values into its stage; `whole`: every key is there
-  auto issue = [&](const char* head, uint8_t* stage, int key, const Pages& t, bool whole) __attribute__((always_inline)) {
-    auto direct = [&](auto check) __attribute__((always_inline)) {
+  auto issue = [&](const char* head, uint32_t stage, int key, const Pages& t) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const char* const src = head + t.id[kPer * i / 8] * P.page + ((key + kPer * i) & mask) * P.slot;
-        const int piece = load_piece ^ swizzle<DP>(kPer * i + load_row);
-        if (!decltype(check)::value || 8 * piece < A.dim)
-          __builtin_amdgcn_global_load_lds(src + (uint32_t)(lane_at + 16 * piece),
-                                           (__attribute__((address_space(3))) void*)(stage + 1024 * i), 16, 0, 0);
-      }
-    };
-    if (whole && !padded) {
-      direct(std::false_type());
-    } else if (whole) {
-      direct(std::true_type());
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < kLoads; ++i) {
-        const int row = kPer * i + load_row, piece = load_piece ^ swizzle<DP>(row), eight = kPer * i / 8;
-        const int page = eight == 0 ? t.id[0] : eight == 1 ? t.id[1] : eight == 2 ? t.id[2] : t.id[3];
-        const char* const src = head + page * P.page + ((key + kPer * i) & mask) * P.slot + lane_at + 16 * piece;
-        const bool in = key + row < sight.most && (t.good >> eight & 1) && 8 * piece < A.dim;
-        *(u32x4*)(stage + 1024 * i + 16 * lane) = in ? *(const u32x4*)src : u32x4{0, 0, 0, 0};
-      }
+    for (int i = 0; i < kLoads; ++i) {
+      const char* const src = head + t.id[kPer * i / 8] * P.page + ((key + kPer * i) & mask) * P.slot;
+      const int piece = load_piece ^ swizzle<DP>(kPer * i + load_row);
+      if (!padded || 8 * piece < A.dim) load_to_lds(stage + 1024 * i, src, lane_at + 16 * piece);
     }
-  };
-  auto is_whole = [&](int key, const Pages& t) __attribute__((always_inline)) {
-    return key + 32 <= sight.most && t.good == 15;
   };
   // this wave's loads have landed but for the last `kLeft`, and its LDS reads have come back
   auto landed = [&](bool more) __attribute__((always_inline)) {
@@ -367,6 +421,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
     __asm__ volatile("" ::: "memory");
   };
 
+  bool odd = false;
   f32x4 o[NT][DP / 16];
   float m[NT], l[NT];
 #pragma unroll
@@ -376,26 +431,15 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
 #pragma unroll
     for (int d = 0; d < DP / 16; ++d) o[n][d] = f32x4{0, 0, 0, 0};
   }
-  int key = from + 32 * w;
   const uint8_t* const k_at = ks + r16 * kRowBytes + 16 * (g ^ swizzle<DP>(r16));
   const int v_row = 4 * g + (r16 >> 2);
   const uint8_t* const v_at = vs + v_row * kRowBytes + 16 * (((lane & 3) >> 1) ^ swizzle<DP>(v_row)) + 8 * (lane & 1);
   if (key < to) {
-    Pages here = lookup(key);
-    bool whole = is_whole(key, here);
-    issue(k_head, ks, key, here, whole);
-    issue(v_head, vs, key, here, whole);
-    // the queries and what the tree says have come back: the loop waits for no loads but its own
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int s = 0; s < DP / 32; ++s) __asm__ volatile("" : "+v"(q[n][s]));
-      __asm__ volatile("" : "+v"(word[n]));
-    }
+    issue(k_head, k_lds, key, here);
+    issue(v_head, v_lds, key, here);
     for (; key < to; key += 32 * W) {
       const bool more = key + 32 * W < to;
       const Pages next = lookup(more ? key + 32 * W : key);
-      const bool next_whole = is_whole(key + 32 * W, next);
       landed(true);  // the keys; the values may be under way
       f32x4 st[NT][2];
 #pragma unroll
@@ -411,8 +455,8 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
         }
       }
       reads_done();
-      if (more) issue(k_head, ks, key + 32 * W, next, next_whole);
-      const bool masked = key + 32 > sight.full || !whole;
+      if (more) issue(k_head, k_lds, key + 32 * W, next);
+      const bool masked = key + 32 > sight.full || here.there != ~0u;
       u32x4 pr[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -420,7 +464,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = st[n][i >> 2][i & 3];
         if (masked) {
-          const uint32_t v = seen(n, key, here.good) >> (4 * g);
+          const uint32_t v = seen(n, key, here.there) >> (4 * g);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (!(v >> (16 * (i >> 2) + (i & 3)) & 1)) x[i] = -INFINITY;
@@ -448,44 +492,12 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
         for (int i = 0; i < 4; ++i) pr[n][i] = Pair<T>::pack(x[2 * i], x[2 * i + 1]);
       }
       landed(more);  // the values; the next keys may be under way
-      if (masked) {
-        // a NaN or an infinity among the values of a key that some rows do not see: its product with their 0
-        // would be one too.  It is added to the rows that see it, and taken out of the stage.
-        uint32_t odd = 0;
+      if (__builtin_expect(here.there != ~0u, 0)) {  // values that are none
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const u32x4 v = *(const u32x4*)(vs + 1024 * i + 16 * lane);
-          const uint64_t b = __ballot(odd_word<T>(v[0]) || odd_word<T>(v[1]) || odd_word<T>(v[2]) || odd_word<T>(v[3]));
-#pragma unroll
-          for (int j = 0; j < kPer; ++j)
-            if (b >> (j * kPieces) & (kPieces == 64 ? ~0ull : (1ull << kPieces) - 1)) odd |= 1u << (kPer * i + j);
-        }
-        if (odd) {
-          for (uint32_t left = odd; left; left &= left - 1) {
-            const int row = __builtin_ctz(left);
-#pragma unroll
-            for (int d = 0; d < DP / 16; ++d) {
-              const u32x2 v = *(const u32x2*)(vs + row * kRowBytes + 16 * ((2 * d + (g >> 1)) ^ swizzle<DP>(row)) + 8 * (g & 1));
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t e16 = v[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
-                const float f = Pair<T>::lo(e16);
-                if (!odd_word<T>(e16)) continue;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  if (seen(n, key, here.good) >> row & 1) o[n][d][e] += f;
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kLoads; ++i) {
-            u32x4 v = *(const u32x4*)(vs + 1024 * i + 16 * lane);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = even_word<T>(v[e]);
-            *(u32x4*)(vs + 1024 * i + 16 * lane) = v;
-          }
-        }
+        for (int i = 0; i < kLoads; ++i)
+          if (!(here.there >> (kPer * i + load_row) & 1)) *(u32x4*)(vs + 1024 * i + 16 * lane) = u32x4{0, 0, 0, 0};
       }
+      if (min(key + 32, sight.most) > sight.full) odd |= clear_odd<T, kLoads>(vs);
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d) {
         const uint8_t* const at = vs + (((int)(v_at - vs)) ^ (32 * d));
@@ -495,9 +507,28 @@ __global__ __launch_bounds__(64 * W) void lb_attn_stream_kernel(const LbAttnArgs
         for (int n = 0; n < NT; ++n) o[n][d] = mfma16<T>(v, pr[n], o[n][d]);
       }
       reads_done();
-      if (more) issue(v_head, vs, key + 32 * W, next, next_whole);
+      if (more) issue(v_head, v_lds, key + 32 * W, next);
       here = next;
-      whole = next_whole;
+    }
+  }
+
+  if (__builtin_expect(odd, 0)) {
+    const int seen_whole = (max(sight.full, from) - from) / 32 * 32;  // steps before are this wave's or not, but seen whole
+#pragma unroll 1
+    for (int at = from + seen_whole; at < to; at += 32) {
+      if ((at - from) / 32 % W != w) continue;
+      const Pages t = lookup(at);
+#pragma unroll 1
+      for (int r = 0; r < 32; ++r) {
+        const int eight = r >> 3, id = eight == 0 ? t.id[0] : eight == 1 ? t.id[1] : eight == 2 ? t.id[2] : t.id[3];
+        const char* const src = v_head + id * P.page + ((at + r) & mask) * P.slot;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const bool mine = seen(n, at, t.there) >> r & 1;
+#pragma unroll
+          for (int d = 0; d < DP / 16; ++d) o[n][d] += odd_values<T>(src, 16 * d + 4 * g, A.dim, mine);
+        }
+      }
     }
   }
 
@@ -552,12 +583,6 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
 }
 
-// 16 bytes a lane from base + offset to LDS, 1 KB from `lds` on.  In assembly, so that the compiler does not wait for it
-// before reads of other stages; the kernel waits itself.  Nothing is loaded into registers.
-__device__ __forceinline__ void load_to_lds(uint32_t lds, const void* base, uint32_t offset) {
-  __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base) : "memory", "m0");
-}
-
 template <typename T, int DP, int RT, int KT, int W>
 __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A) {
   constexpr int kRowBytes = 2 * DP, kPieces = DP / 8, kKeys = 32 * KT, kStage = kKeys * kRowBytes;
@@ -566,6 +591,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   constexpr int kRows = 32 * RT * W, kS = DP / 16, kD = DP / 32;
   static_assert(kPer <= 8 && kLoads * 1024 * W == kStage, "a load lies in one page");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[5 * kStage];
+  __shared__ int odd_waves[W];
   const int w = wave_id(), lane = threadIdx.x & 63;
   const int r32 = lane & 31, h = lane >> 5;
   const int kv_head = blockIdx.x % A.kv_heads;
@@ -588,8 +614,6 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   const LbPages& P = A.pages;
   const char* const k_head = P.k + kv_head * P.head;
   const char* const v_head = P.v + kv_head * P.head;
-  uint8_t* const k_lds = lds;
-  uint8_t* const v_lds = lds + 2 * kStage;
   const bool padded = A.dim < DP;
   if (padded) {  // pieces that no load fills
     for (int i = threadIdx.x; i < 5 * kStage / 16; i += 64 * W) *(u32x4*)(lds + 16 * i) = u32x4{0, 0, 0, 0};
@@ -604,7 +628,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   for (int n = 0; n < RT; ++n) {
     const int row = first_row + 32 * n + r32;
     const bool in = row < all_rows;
-    const int t = in ? row / A.group : 0, head = kv_head * A.group + (in ? row - t * A.group : 0);
+    const int t = in ? (uint32_t)row / (uint32_t)A.group : 0, head = kv_head * A.group + (in ? row - t * A.group : 0);
     const T* src = (const T*)A.q + (p.s.start + t) * A.qt + head * A.qh;
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
@@ -620,59 +644,50 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   const int mask = (1 << P.shift) - 1;
   auto page_at = [&](int key) __attribute__((always_inline)) { return table[min(key >> P.shift, P.columns - 1)]; };
   auto is_page = [&](int page) __attribute__((always_inline)) { return (uint32_t)page < (uint32_t)P.pages; };
+  // whether every key has a page: most steps do not ask again
+  bool some = false;
+  for (int c = (from >> P.shift) + lane; c <= (to - 1) >> P.shift; c += 64) some = some || !is_page(P.table[p.seq * P.table_stride + c]);
+  const bool good = __ballot(some) == 0;
   // this wave's part of tile t's keys and values into their stages
   const int load_row = lane / kPieces, load_piece = lane % kPieces;
   auto fill = [&](int t) __attribute__((always_inline)) {
     const int key0 = from + t * kKeys;
-    uint8_t* const k_to = k_lds + (t & 1) * kStage;
-    uint8_t* const v_to = v_lds + (t % 3) * kStage;
-    int page[kLoads];
-    bool whole = key0 + kKeys <= sight.most;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      page[i] = page_at(key0 + kPer * (kLoads * w + i));
-      whole = whole && is_page(page[i]);
-    }
+    const uint32_t k_to = lds_address(lds) + (t & 1) * kStage, v_to = lds_address(lds) + (2 + t % 3) * kStage;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int at = kPer * (kLoads * w + i), row = at + load_row, piece = load_piece ^ swizzle<DP>(row);
-      const long src = page[i] * P.page + ((key0 + at) & mask) * P.slot;
+      const int page = page_at(key0 + at);
+      const long src = (is_page(page) ? page : 0) * P.page + ((key0 + at) & mask) * P.slot;
       const uint32_t offset = load_row * (int)P.slot + 16 * piece;
-      if (whole) {
-        if (!padded || 8 * piece < A.dim) {
-          load_to_lds((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)k_to + at * kRowBytes, k_head + src, offset);
-          load_to_lds((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)v_to + at * kRowBytes, v_head + src, offset);
-        }
-      } else {
-        const bool in = key0 + row < sight.most && is_page(page[i]) && 8 * piece < A.dim;
-        u32x4 k = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-        if (in) {
-          k = *(const u32x4*)(k_head + src + offset);
-          v = *(const u32x4*)(v_head + src + offset);
-        }
-        *(u32x4*)(k_to + at * kRowBytes + 16 * lane) = k;
-        *(u32x4*)(v_to + at * kRowBytes + 16 * lane) = v;
+      if (!padded || 8 * piece < A.dim) {
+        load_to_lds(k_to + at * kRowBytes, k_head + src, offset);
+        load_to_lds(v_to + at * kRowBytes, v_head + src, offset);
       }
     }
   };
-  // the tile that was asked for has landed, in all waves, and every wave is past the stages that come next
-  auto meet = [&]() __attribute__((always_inline)) {
-    __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  bool odd = false;
+  // tile t, that was asked for, has landed in all waves, and every wave is past the stages that come next
+  auto meet = [&](int t) __attribute__((always_inline)) {
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int key0 = from + t * kKeys;
+    if (__builtin_expect(!good || key0 + kKeys > sight.most, 0)) {  // values that are none
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int at = kPer * (kLoads * w + i);
+        if (key0 + at + load_row >= sight.most || !is_page(page_at(key0 + at)))
+          *(u32x4*)(lds + (2 + t % 3) * kStage + at * kRowBytes + 16 * lane) = u32x4{0, 0, 0, 0};
+      }
+    }
+    if (min(key0 + kKeys, sight.most) > sight.full)
+      odd |= clear_odd<T, kLoads>(lds + (2 + t % 3) * kStage + kPer * kLoads * w * kRowBytes);
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
   };
 
   // which of a step's keys row n sees
-  auto below = [](int n) __attribute__((always_inline)) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
   auto seen = [&](int n, int key, uint32_t there) __attribute__((always_inline)) {
-    uint32_t v = below(sees[n] - key) & there;
-    if (A.tree) {
-      const int before = p.s.base - key;
-      const uint32_t drafted = before >= 32 ? 0u : before >= 0 ? (uint32_t)(word[n] << before)
-                               : before > -64 ? (uint32_t)(word[n] >> -before) : 0u;
-      v &= below(before) | drafted;
-    }
-    return v;
+    return seen_of(A, p.s.base, key, there, sees[n], word[n]);
   };
   // keys of a step that have a page, a bit each
   auto paged = [&](int key) __attribute__((always_inline)) {
@@ -729,53 +744,6 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
       }
     }
   };
-  // The same where a key that some rows do not see has a NaN or an infinity among its values: they are added to the
-  // rows that see it, and left out of the products.
-  auto odd_keys = [&](int j) __attribute__((always_inline)) {
-    uint32_t odd = 0;
-    const int at = v_of(j);
-#pragma unroll
-    for (int i = 0; i < 32 / kPer; ++i) {
-      const u32x4 v = *(const u32x4*)(lds + at + 1024 * i + 16 * lane);
-      const uint64_t b = __ballot(odd_word<T>(v[0]) || odd_word<T>(v[1]) || odd_word<T>(v[2]) || odd_word<T>(v[3]));
-#pragma unroll
-      for (int e = 0; e < kPer; ++e)
-        if (b >> (e * kPieces) & (1ull << kPieces) - 1) odd |= 1u << (kPer * i + e);
-    }
-    return odd;
-  };
-  auto odd_products = [&](int j, uint32_t odd, uint32_t t) __attribute__((always_inline)) {
-    const int at = v_of(j), key = from + 32 * j;
-    for (uint32_t left = odd; left; left &= left - 1) {
-      const int row = __builtin_ctz(left);
-#pragma unroll
-      for (int d = 0; d < kD; ++d) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const u32x2 v = *(const u32x2*)(lds + at + row * kRowBytes + 16 * ((4 * d + i) ^ swizzle<DP>(row)) + 8 * h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t e16 = v[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
-            if (!odd_word<T>(e16)) continue;
-#pragma unroll
-            for (int n = 0; n < RT; ++n)
-              if (seen(n, key, t) >> row & 1) o[n][d][4 * i + e] += Pair<T>::lo(e16);
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int d = 0; d < kD; ++d) {
-        const u32x2 v0 = read_transposed(lds + ((at + v_at) ^ (64 * d)) + 16 * s * kRowBytes);
-        const u32x2 v1 = read_transposed(lds + ((at + v_at) ^ (64 * d) ^ 32) + (16 * s + 8) * kRowBytes);
-        const u32x4 v = {even_word<T>(v0[0]), even_word<T>(v0[1]), even_word<T>(v1[0]), even_word<T>(v1[1])};
-#pragma unroll
-        for (int n = 0; n < RT; ++n) o[n][d] = mfma32<T>(v, pr[n][s], o[n][d]);
-      }
-    }
-  };
   // the largest score of each row so far
   auto maxima = [&](const f32x16 (&s)[RT], float (&most)[RT]) __attribute__((always_inline)) {
 #pragma unroll
@@ -822,18 +790,15 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   auto advance = [&](int j) __attribute__((always_inline)) {
     const int t = (j + 1) / KT;
     if ((j + 1) % KT == 0 && t < tiles) {
-      meet();
+      meet(t);
       if (t + 1 < tiles) fill(t + 1);
     }
   };
 
   if (tiles > 0) {
     fill(0);
-    // whether every key has a page: the loop below does not ask again
-    bool good = true;
-    for (int c = (from >> P.shift) + lane; c <= (to - 1) >> P.shift; c += 64) good = good && is_page(P.table[p.seq * P.table_stride + c]);
-    const int clear = __ballot(!good) ? 0 : min(steps, (min(own.full, to) - from) >> 5);  // steps that all rows see whole
-    meet();
+    const int clear = good ? min(steps, (min(own.full, to) - from) >> 5) : 0;  // steps that all rows see whole
+    meet(0);
     if (tiles > 1) fill(1);
     float most[RT];
     int j = 0;
@@ -882,14 +847,39 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
       maxima(st[0], most);
       rescale(most);
       probabilities(st[0]);
-      const uint32_t odd = odd_keys(j);
-      if (odd)
-        odd_products(j, odd, there);
-      else
-        products(j);
+      products(j);
       advance(j);
     }
     for (; j < tiles * KT; ++j) advance(j);
+    if (lane == 0) odd_waves[w] = odd;
+    __syncthreads();
+    odd = false;
+#pragma unroll
+    for (int i = 0; i < W; ++i) odd = odd || odd_waves[i];
+    if (__builtin_expect(odd, 0)) {
+      // from the first tile on in which some were cleared
+#pragma unroll 1
+      for (int at = from + (max(sight.full, from) - from) / kKeys * kKeys; at < to; at += 32) {
+        const uint32_t there = paged(at);
+#pragma unroll 1
+        for (int r = 0; r < 32; ++r) {
+          const int page = page_at(at + r);
+          const char* const src = v_head + (is_page(page) ? page : 0) * P.page + ((at + r) & mask) * P.slot;
+#pragma unroll
+          for (int n = 0; n < RT; ++n) {
+            const bool mine = seen(n, at, there) >> r & 1;
+#pragma unroll
+            for (int d = 0; d < kD; ++d)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const f32x4 f = odd_values<T>(src, 32 * d + 8 * i + 4 * h, A.dim, mine);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][d][4 * i + e] += f[e];
+              }
+          }
+        }
+      }
+    }
   }
 #pragma unroll
   for (int n = 0; n < RT; ++n) {
