@@ -129,16 +129,16 @@ _empty = torch.empty_strided
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _ref = ctypes.byref
 _recording = torch.is_grad_enabled
+_current = torch._C._cuda_getDevice
 
 
-def _on(device, stream):
-    """(context, stream pointer): `device` current, allocations on `stream`."""
+def _on(index, stream):
+    """(context, stream pointer): device `index` current, allocations on `stream`."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{index}")
         return torch.cuda.stream(stream), int(stream.cuda_stream)
-    index = device.index
-    return (_HERE if index == torch.cuda.current_device() else torch.cuda.device(index)), _raw_stream(index)
+    return (_HERE if index == _current() else torch.cuda.device(index)), _raw_stream(index)
 
 
 def _keep(stream, *tensors):
@@ -156,56 +156,70 @@ def _no_history(*tensors):
                              "autograd; call under torch.no_grad() and take the gradient by littlebit_rope_bwd")
 
 
+# The checks ask for everything at once, and for the reason only where something is wrong: these calls are short.
+
 def _first(name: str, t: torch.Tensor):
-    """(type code, device) of the tensor that the others are held to."""
+    """(type code, device index) of the tensor that the others are held to."""
     code = _HALF.get(t.dtype) if torch.is_tensor(t) else None
     if code is None:
         raise ValueError(f"{name} must be a tensor of {' or '.join(str(d) for d in _HALF)}")
-    if t.dim() != 3 or not t.is_cuda:
+    index = t.get_device()
+    if index < 0 or t.dim() != 3:
         raise ValueError(f"{name} must be a tokens x heads x dim CUDA tensor")
-    return code, t.device
+    return code, index
 
 
-def _heads(name: str, t: torch.Tensor, dtype, device, tokens: int, dim: int, heads: Optional[int] = None) -> _Heads:
-    if not torch.is_tensor(t) or t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{name} must be a tokens x heads x dim CUDA tensor")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call is on {device}")
-    n, h, d = t.shape
-    if n != tokens or d != dim or (heads is not None and h != heads):
-        raise ValueError(f"{name} must have shape ({tokens}, {h if heads is None else heads}, {dim}), has {tuple(t.shape)}")
-    st, sh, sd = t.stride()
-    if sd != 1 and dim > 1:
-        raise ValueError(f"the channels of {name} must lie together")
-    return _Heads(t.data_ptr(), st, sh, h)
+def _heads(name: str, t: torch.Tensor, dtype, index: int, tokens: int, dim: int, heads: int = 0) -> _Heads:
+    """A tokens x heads x dim argument; any number of heads for heads = 0."""
+    if torch.is_tensor(t) and t.dim() == 3:
+        n, h, d = t.shape
+        st, sh, sd = t.stride()
+        if n == tokens and d == dim and t.dtype is dtype and t.get_device() == index and (h == heads or not heads) \
+                and (sd == 1 or d == 1):
+            return _Heads(t.data_ptr(), st, sh, h)
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, is {t.dtype}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the call is on cuda:{index}")
+        if n == tokens and d == dim and (h == heads or not heads):
+            raise ValueError(f"the channels of {name} must lie together")
+        raise ValueError(f"{name} must have shape ({tokens}, {heads or h}, {dim}), has {tuple(t.shape)}")
+    raise ValueError(f"{name} must be a tokens x heads x dim CUDA tensor")
 
 
-def _ints(name: str, t: torch.Tensor, device, n: int, dtype=torch.int32) -> int:
-    if not torch.is_tensor(t) or t.dtype is not dtype or t.device != device or t.dim() != 1:
-        raise ValueError(f"{name} must be a 1-D {dtype} tensor on {device}")
-    if t.shape[0] != n or not t.is_contiguous():
+def _ints(name: str, t: torch.Tensor, index: int, n: int, dtype=torch.int32) -> int:
+    if torch.is_tensor(t) and t.dtype is dtype and t.get_device() == index and t.dim() == 1:
+        if t.shape[0] == n and t.is_contiguous():
+            return t.data_ptr()
         raise ValueError(f"{name} must be {n} contiguous values")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a 1-D {dtype} tensor on cuda:{index}")
 
 
-def _rope(positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, device, tokens, dim) -> _Rope:
-    rot = pos = inv = 0
+def _rope(positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, index, tokens, dim) -> _Rope:
+    half, pos, inv = 0, None, None
     if inv_freq is not None:
-        rot = 2 * inv_freq.shape[0] if torch.is_tensor(inv_freq) and inv_freq.dim() == 1 else 0
-        inv = _ints("inv_freq", inv_freq, device, rot // 2, torch.float32)
+        half = inv_freq.shape[0] if torch.is_tensor(inv_freq) and inv_freq.dim() == 1 else 0
+        inv = _ints("inv_freq", inv_freq, index, half, torch.float32)
         if positions is None:
             raise ValueError("inv_freq needs positions")
-        pos = _ints("positions", positions, device, tokens)
-    weights = []
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        weights.append(None if w is None else _ints(name, w, device, dim, dtype))
-    return _Rope(pos or None, inv or None, rot, int(bool(interleaved)), weights[0], weights[1], eps)
+        pos = _ints("positions", positions, index, tokens)
+    return _Rope(pos, inv, 2 * half, 1 if interleaved else 0,
+                 None if q_weight is None else _ints("q_weight", q_weight, index, dim, dtype),
+                 None if k_weight is None else _ints("k_weight", k_weight, index, dim, dtype), eps)
 
 
-def _new_heads(tokens, heads, dim, dtype, device) -> torch.Tensor:
-    return _empty((tokens, heads, dim), (heads * dim, dim, 1), dtype=dtype, device=device)
+def _new_heads(tokens, heads, dim, dtype, index):
+    """A new tensor of heads, and its argument."""
+    row = heads * dim
+    t = _empty((tokens, heads, dim), (row, dim, 1), dtype=dtype, device=index)
+    return t, _Heads(t.data_ptr(), row, dim, heads)
+
+
+def _out(name, t, dtype, index, tokens, dim, heads):
+    """An output that is given, or a new one, and its argument."""
+    if t is None:
+        return _new_heads(tokens, heads, dim, dtype, index)
+    return t, _heads(name, t, dtype, index, tokens, dim, heads)
 
 
 # --------------------------------------------------------------------------------------- head norm and rotation
@@ -220,24 +234,22 @@ def littlebit_rope_fwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], pos
     k may be None.  ``q_out`` and ``k_out`` may name the outputs, q and k
     themselves included."""
     one = q if q is not None else k
-    code, device = _first("q" if q is not None else "k", one)
+    code, index = _first("q" if q is not None else "k", one)
     dtype, (tokens, _, dim) = one.dtype, one.shape
-    hq = None if q is None else _heads("q", q, dtype, device, tokens, dim)
-    hk = None if k is None else _heads("k", k, dtype, device, tokens, dim)
+    hq = None if q is None else _heads("q", q, dtype, index, tokens, dim)
+    hk = None if k is None else _heads("k", k, dtype, index, tokens, dim)
     if (q is None and q_out is not None) or (k is None and k_out is not None):
         raise ValueError("an output without its input")
-    rope = _rope(positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, device, tokens, dim)
+    rope = _rope(positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, index, tokens, dim)
     if _recording():
         _no_history(q, k, inv_freq, q_weight, k_weight, q_out, k_out)
-    ctx, sp = _on(device, stream)
+    ctx, sp = _on(index, stream)
     with ctx:
         oq = ok = None
         if q is not None:
-            q_out = _new_heads(tokens, hq.heads, dim, dtype, device) if q_out is None else q_out
-            oq = _heads("q_out", q_out, dtype, device, tokens, dim, hq.heads)
+            q_out, oq = _out("q_out", q_out, dtype, index, tokens, dim, hq.heads)
         if k is not None:
-            k_out = _new_heads(tokens, hk.heads, dim, dtype, device) if k_out is None else k_out
-            ok = _heads("k_out", k_out, dtype, device, tokens, dim, hk.heads)
+            k_out, ok = _out("k_out", k_out, dtype, index, tokens, dim, hk.heads)
         _check(LIB.littlebit_rope_fwd(hq and _ref(hq), hk and _ref(hk), _ref(rope), code, tokens, dim, oq and _ref(oq),
                                       ok and _ref(ok), sp))
     if stream is not None:
@@ -257,38 +269,36 @@ def littlebit_rope_bwd(dq: Optional[torch.Tensor], dk: Optional[torch.Tensor], p
     they are needed with a weight only.  ``dq_in`` and ``dk_in`` may name the
     outputs, dq and dk themselves included."""
     one = dq if dq is not None else dk
-    code, device = _first("dq" if dq is not None else "dk", one)
+    code, index = _first("dq" if dq is not None else "dk", one)
     dtype, (tokens, _, dim) = one.dtype, one.shape
     if dq is None:
         q = q_weight = None
     if dk is None:
         k = k_weight = None
-    hdq = None if dq is None else _heads("dq", dq, dtype, device, tokens, dim)
-    hdk = None if dk is None else _heads("dk", dk, dtype, device, tokens, dim)
+    hdq = None if dq is None else _heads("dq", dq, dtype, index, tokens, dim)
+    hdk = None if dk is None else _heads("dk", dk, dtype, index, tokens, dim)
     if (dq is None and dq_in is not None) or (dk is None and dk_in is not None):
         raise ValueError("an output without its input")
-    rope = _rope(positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, device, tokens, dim)
-    hq = _heads("q", q, dtype, device, tokens, dim, hdq.heads) if q_weight is not None else None
-    hk = _heads("k", k, dtype, device, tokens, dim, hdk.heads) if k_weight is not None else None
+    rope = _rope(positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, index, tokens, dim)
+    hq = _heads("q", q, dtype, index, tokens, dim, hdq.heads) if q_weight is not None else None
+    hk = _heads("k", k, dtype, index, tokens, dim, hdk.heads) if k_weight is not None else None
     if _recording():
         _no_history(dq, dk, q, k, inv_freq, q_weight, k_weight, dq_in, dk_in)
-    ctx, sp = _on(device, stream)
+    ctx, sp = _on(index, stream)
     with ctx:
         oq = ok = dqw = dkw = ws = None
         need = 0
         if dq is not None:
-            dq_in = _new_heads(tokens, hdq.heads, dim, dtype, device) if dq_in is None else dq_in
-            oq = _heads("dq_in", dq_in, dtype, device, tokens, dim, hdq.heads)
+            dq_in, oq = _out("dq_in", dq_in, dtype, index, tokens, dim, hdq.heads)
         if dk is not None:
-            dk_in = _new_heads(tokens, hdk.heads, dim, dtype, device) if dk_in is None else dk_in
-            ok = _heads("dk_in", dk_in, dtype, device, tokens, dim, hdk.heads)
+            dk_in, ok = _out("dk_in", dk_in, dtype, index, tokens, dim, hdk.heads)
         if q_weight is not None:
-            dqw = _empty((dim,), (1,), dtype=torch.float32, device=device)
+            dqw = _empty((dim,), (1,), dtype=torch.float32, device=index)
         if k_weight is not None:
-            dkw = _empty((dim,), (1,), dtype=torch.float32, device=device)
+            dkw = _empty((dim,), (1,), dtype=torch.float32, device=index)
         if dqw is not None or dkw is not None:
             need = LIB.littlebit_rope_bwd_workspace_bytes(tokens, hdq.heads if hdq else 0, hdk.heads if hdk else 0, dim)
-            ws = _empty((need,), (1,), dtype=torch.uint8, device=device)
+            ws = _empty((need,), (1,), dtype=torch.uint8, device=index)
         _check(LIB.littlebit_rope_bwd(
             hdq and _ref(hdq), hdk and _ref(hdk), hq and _ref(hq), hk and _ref(hk), _ref(rope), code, tokens, dim,
             oq and _ref(oq), ok and _ref(ok), None if dqw is None else dqw.data_ptr(),
@@ -316,15 +326,14 @@ class LittleBitCache:
     def c_struct(self) -> _Cache:
         k, v = self.k, self.v
         code = _HALF.get(k.dtype) if torch.is_tensor(k) else None
-        if code is None or not torch.is_tensor(v) or k.dim() != 4 or not k.is_cuda:
+        if code is None or not torch.is_tensor(v) or k.dim() != 4 or k.get_device() < 0:
             raise ValueError("a cache is two pages x heads x slots x dim CUDA tensors of float16 or bfloat16")
-        if v.dtype is not k.dtype or v.device != k.device or v.shape != k.shape or v.stride() != k.stride():
+        strides = k.stride()
+        if v.dtype is not k.dtype or v.get_device() != k.get_device() or v.shape != k.shape or v.stride() != strides:
             raise ValueError("the cache's values must have the keys' type, device, shape and strides")
-        pages, heads, slots, dim = k.shape
-        sp, sh, ss, sd = k.stride()
-        if sd != 1:
+        if strides[3] != 1:
             raise ValueError("the cache's channels must lie together")
-        return _Cache(k.data_ptr(), v.data_ptr(), sp, sh, ss, pages, heads, slots, dim, code)
+        return _Cache(k.data_ptr(), v.data_ptr(), *strides[:3], *k.shape, code)
 
 
 @dataclass
@@ -338,16 +347,15 @@ class CacheBatch:
     lens: torch.Tensor
     table: torch.Tensor
 
-    def c_struct(self, device) -> _Batch:
-        lens, table = self.lens, self.table
-        if not torch.is_tensor(lens) or lens.dim() != 1:
-            raise ValueError(f"lens must be a 1-D torch.int32 tensor on {device}")
-        seqs = lens.shape[0]
-        if not torch.is_tensor(table) or table.dtype is not torch.int32 or table.device != device or table.dim() != 2 \
-                or table.shape[0] != seqs or (table.shape[1] > 1 and table.stride(1) != 1):
-            raise ValueError(f"table must be a torch.int32 tensor of {seqs} rows on {device}, entries of a row together")
-        return _Batch(_ints("starts", self.starts, device, seqs + 1), _ints("lens", lens, device, seqs), table.data_ptr(),
-                      max(table.stride(0), table.shape[1]) if seqs == 1 else table.stride(0), seqs, table.shape[1])
+    def c_struct(self, index: int) -> _Batch:
+        starts, lens, table = self.starts, self.lens, self.table
+        if torch.is_tensor(lens) and torch.is_tensor(table) and lens.dim() == 1 and table.dim() == 2:
+            seqs, columns = table.shape
+            stride, one = table.stride()
+            if table.dtype is torch.int32 and table.get_device() == index and (one == 1 or columns == 1):
+                return _Batch(_ints("starts", starts, index, seqs + 1), _ints("lens", lens, index, seqs), table.data_ptr(),
+                              stride if seqs > 1 else columns, seqs, columns)
+        raise ValueError(f"lens must be a 1-D and table a 2-D torch.int32 tensor on cuda:{index}, entries of a row together")
 
 
 def littlebit_cache_append(cache: LittleBitCache, batch: CacheBatch, k: torch.Tensor, v: torch.Tensor,
@@ -359,24 +367,23 @@ def littlebit_cache_append(cache: LittleBitCache, batch: CacheBatch, k: torch.Te
     the batch's rows into its pages; returns the queries, normed and turned (None
     without q).  ``q_out`` may name that output, q itself included."""
     c = cache.c_struct()
-    dtype, device, dim = cache.k.dtype, cache.k.device, c.dim
-    b = batch.c_struct(device)
+    dtype, index, dim = cache.k.dtype, cache.k.get_device(), c.dim
+    b = batch.c_struct(index)
     _first("k", k)
     tokens = k.shape[0]
-    hk = _heads("k", k, dtype, device, tokens, dim, c.heads)
-    hv = _heads("v", v, dtype, device, tokens, dim, c.heads)
-    hq = None if q is None else _heads("q", q, dtype, device, tokens, dim)
+    hk = _heads("k", k, dtype, index, tokens, dim, c.heads)
+    hv = _heads("v", v, dtype, index, tokens, dim, c.heads)
+    hq = None if q is None else _heads("q", q, dtype, index, tokens, dim)
     if q is None and (q_out is not None or q_weight is not None):
         raise ValueError("q_out and q_weight need q")
-    rope = _rope(positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, device, tokens, dim)
+    rope = _rope(positions, inv_freq, q_weight, k_weight, eps, interleaved, dtype, index, tokens, dim)
     if _recording():
         _no_history(cache.k, cache.v, k, v, q, inv_freq, q_weight, k_weight, q_out)
-    ctx, sp = _on(device, stream)
+    ctx, sp = _on(index, stream)
     with ctx:
         oq = None
         if q is not None:
-            q_out = _new_heads(tokens, hq.heads, dim, dtype, device) if q_out is None else q_out
-            oq = _heads("q_out", q_out, dtype, device, tokens, dim, hq.heads)
+            q_out, oq = _out("q_out", q_out, dtype, index, tokens, dim, hq.heads)
         _check(LIB.littlebit_cache_append(_ref(c), _ref(b), tokens, _ref(hk), _ref(hv), hq and _ref(hq), _ref(rope),
                                           oq and _ref(oq), sp))
     if stream is not None:
@@ -396,23 +403,22 @@ def littlebit_cache_attention_fwd(q: torch.Tensor, cache: LittleBitCache, batch:
     default.  ``lse`` (fp32, tokens x heads) receives the logarithm of each row's
     sum of exponentials."""
     c = cache.c_struct()
-    dtype, device, dim = cache.k.dtype, cache.k.device, c.dim
-    b = batch.c_struct(device)
+    dtype, index, dim = cache.k.dtype, cache.k.get_device(), c.dim
+    b = batch.c_struct(index)
     _first("q", q)
     tokens, heads = q.shape[0], q.shape[1]
-    hq = _heads("q", q, dtype, device, tokens, dim)
-    word = None if tree is None else _ints("tree", tree, device, tokens, torch.int64)
-    if lse is not None and (not torch.is_tensor(lse) or lse.dtype is not torch.float32 or lse.device != device
+    hq = _heads("q", q, dtype, index, tokens, dim)
+    word = None if tree is None else _ints("tree", tree, index, tokens, torch.int64)
+    if lse is not None and (not torch.is_tensor(lse) or lse.dtype is not torch.float32 or lse.get_device() != index
                             or lse.shape != (tokens, heads) or not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous torch.float32 tensor of shape {(tokens, heads)} on {device}")
+        raise ValueError(f"lse must be a contiguous torch.float32 tensor of shape {(tokens, heads)} on cuda:{index}")
     if _recording():
         _no_history(cache.k, cache.v, q, out, lse)
-    ctx, sp = _on(device, stream)
+    ctx, sp = _on(index, stream)
     with ctx:
-        out = _new_heads(tokens, heads, dim, dtype, device) if out is None else out
-        ho = _heads("out", out, dtype, device, tokens, dim, heads)
+        out, ho = _out("out", out, dtype, index, tokens, dim, heads)
         need = LIB.littlebit_cache_attention_workspace_bytes(_ref(c), _ref(b), tokens, heads)
-        ws = _empty((need,), (1,), dtype=torch.uint8, device=device)
+        ws = _empty((need,), (1,), dtype=torch.uint8, device=index)
         _check(LIB.littlebit_cache_attention_fwd(
             _ref(c), _ref(b), tokens, _ref(hq), word, 1.0 / math.sqrt(dim) if scale is None else scale, _ref(ho),
             None if lse is None else lse.data_ptr(), ws.data_ptr() if need else None, need, sp))
@@ -426,14 +432,14 @@ def littlebit_cache_accept(cache: LittleBitCache, batch: CacheBatch, path: torch
     keys and values of row path[i][j] to the place of row j; negative entries end
     or skip.  path is int32, one row a sequence."""
     c = cache.c_struct()
-    device = cache.k.device
-    b = batch.c_struct(device)
-    if not torch.is_tensor(path) or path.dtype is not torch.int32 or path.device != device or path.dim() != 2 \
+    index = cache.k.get_device()
+    b = batch.c_struct(index)
+    if not torch.is_tensor(path) or path.dtype is not torch.int32 or path.get_device() != index or path.dim() != 2 \
             or path.shape[0] != b.seqs or not path.is_contiguous():
-        raise ValueError(f"path must be a contiguous torch.int32 tensor of {b.seqs} rows on {device}")
+        raise ValueError(f"path must be a contiguous torch.int32 tensor of {b.seqs} rows on cuda:{index}")
     if _recording():
         _no_history(cache.k, cache.v)
-    ctx, sp = _on(device, stream)
+    ctx, sp = _on(index, stream)
     with ctx:
         _check(LIB.littlebit_cache_accept(_ref(c), _ref(b), path.data_ptr(), path.shape[1], sp))
     if stream is not None:
