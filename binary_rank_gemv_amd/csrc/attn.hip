@@ -14,6 +14,7 @@
 // that about `target` workgroups share them, whatever the lengths; a sequence's parts
 // are joined by a second kernel.  All of that is computed on the device, so that a captured call
 // serves any lengths.
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_common.h"
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
   const int first_row = block * kRows, all_rows = p.s.rows * A.group;
   const Sight sight = sight_of(A, p.s, first_row, kRows);
   const int parts = parts_of(sight.most, p.span);
-  if (part >= parts) return;
+  if (part >= parts || (parts > 1 && p.slot >= A.slots)) return;  // the latter: starts that name rows twice
   const int from = part * p.span, to = min(from + p.span, sight.most);
 
   const LbPages& P = A.pages;
@@ -591,7 +592,6 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   constexpr int kRows = 32 * RT * W, kS = DP / 16, kD = DP / 32;
   static_assert(kPer <= 8 && kLoads * 1024 * W == kStage, "a load lies in one page");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[5 * kStage];
-  __shared__ int odd_waves[W];
   const int w = wave_id(), lane = threadIdx.x & 63;
   const int r32 = lane & 31, h = lane >> 5;
   const int kv_head = blockIdx.x % A.kv_heads;
@@ -602,7 +602,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   const int all_rows = p.s.rows * A.group;
   const Sight sight = sight_of(A, p.s, block * kRows, kRows);
   const int parts = parts_of(sight.most, p.span);
-  if (part >= parts) return;
+  if (part >= parts || (parts > 1 && p.slot >= A.slots)) return;  // the latter: starts that name rows twice
   const int from = part * p.span, to = min(from + p.span, sight.most);
   const int first_row = block * kRows + 32 * RT * w;
   // this wave's own rows: their keys end earlier, and may be seen by all of them later
@@ -851,6 +851,8 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
       advance(j);
     }
     for (; j < tiles * KT; ++j) advance(j);
+    __syncthreads();  // the stages have been read
+    int* const odd_waves = (int*)lds;
     if (lane == 0) odd_waves[w] = odd;
     __syncthreads();
     odd = false;
@@ -899,8 +901,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
 
 // ------------------------------------------------------------------------- the join
 // Rows of the call whose keys were taken in parts.  A wave looks at `per` rows' records at once and joins those
-// with several parts, one after the other: all parts' maxima first, 64 at a time, then their sums, four channels a lane
-// and 64 / LD parts at a time.  A part in which a row saw nothing has no maximum, and a sum of 0 (or NaN).
+// with several parts, one after the other: eight times 64 / LD parts at once, four channels a lane.  A part in which a row saw nothing has no maximum, and a sum of 0 (or NaN).
 template <typename T, int LD>
 __global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, int rows, int per) {
   constexpr int kSets = 64 / LD;
@@ -924,16 +925,8 @@ __global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, i
   for (uint64_t left = __ballot(several); left; left &= left - 1) {
     const int l = __builtin_ctzll(left);
     const int first = __builtin_amdgcn_readlane(r.first, l), count = __builtin_amdgcn_readlane(r.count, l);
-    float top = -INFINITY;
-    for (int j = 0; j < count; j += 64) top = fmaxf(top, lane + j < count ? ws.ml[first + (lane + j) * step].x : -INFINITY);
-    top = fmaxf(top, lane_xor<1>(top));
-    top = fmaxf(top, lane_xor<2>(top));
-    top = fmaxf(top, lane_xor<4>(top));
-    top = fmaxf(top, lane_xor<8>(top));
-    top = fmaxf(top, lane_xor<16>(top));
-    top = fmaxf(top, lane_xor<32>(top));
+    float top = -INFINITY, total = 0.0f;
     f32x4 sum = {0, 0, 0, 0};
-    float total = 0.0f;
     // eight sets' loads at a time; behind the last part it again, with factor 0
 #pragma unroll 1
     for (int j = 0; j < count; j += 8 * kSets) {
@@ -944,6 +937,17 @@ __global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, i
         const int at = first + min(j + kSets * i + set, count - 1) * step;
         v[i] = ws.ml[at];
         o[i] = in ? *(const f32x4*)(ws.sums + (long)at * A.dim + d) : f32x4{0, 0, 0, 0};
+      }
+      float most = top;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = fmaxf(most, v[i].x);
+      if constexpr (LD <= 16) most = fmaxf(most, lane_xor<16>(most));
+      if constexpr (LD <= 32) most = fmaxf(most, lane_xor<32>(most));
+      const float before = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - most);
+      top = most;
+      if (j > 0) {  // what has been added so far: of parts without a maximum it is 0 or NaN, and stays that
+        total *= before;
+        sum *= before;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -1028,12 +1032,17 @@ LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int64_t capacity, int heads, i
   p.rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 && dim <= 128 ? 64 : dim <= 128 ? 256 : 128;
   // workgroups at once: by their LDS and registers
   p.round = p.rows > 64 ? 256 : dim <= 64 && p.rows == 16 ? 1024 : 512;
-  p.target = p.rows > 64 ? 512 : p.rows == 16 ? 1536 : 1024;
   p.least = p.rows > 64 ? 2048 : 256;
-  p.join = capacity > p.least;
-  const int64_t share = (p.target + kv_heads - 1) / kv_heads;
-  p.slots = p.join ? 2 * share + 8 : 0;
-  p.grid = (share + tokens * group / p.rows + seqs + 8) * kv_heads;
+  // blocks of all sequences, at most, and what is shared out for so many; an empty workgroup costs a nanosecond (6000 of
+  // them for one token 5 us)
+  const int64_t blocks = std::min(tokens * group / p.rows + seqs, tokens * group);
+  const int64_t most = p.rows > 64 ? 512 : p.rows == 16 ? 1536 : 1024;
+  p.target = (int)std::min<int64_t>(most, p.round * (1 + 4 * blocks * kv_heads / p.round));
+  const int64_t parts = (capacity + p.least - 1) / p.least;
+  p.join = parts > 1;
+  const int64_t share = (p.target + kv_heads - 1) / kv_heads + 1;
+  p.slots = p.join ? std::min(2 * share + 2, blocks * parts) : 0;
+  p.grid = std::min(share + blocks + 2, blocks * parts) * kv_heads;
   return p;
 }
 
