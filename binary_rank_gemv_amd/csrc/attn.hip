@@ -806,13 +806,89 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
       scores(0, st[0]);
       maxima(st[0], most);
       rescale(most);
+      // A step's instructions in the order they are wanted: reads well ahead of their products, and between the products
+      // the exponentials and the maxima.  Nothing is moved across a fence.
+      auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
       auto body = [&](auto parity, int j) __attribute__((always_inline)) {
         constexpr int B = decltype(parity)::value;
         advance(j);
-        scores(j + 1, st[1 - B]);
-        probabilities(st[B]);
-        products(j);
-        maxima(st[1 - B], most);
+        u32x4 kf[kS], vf[2 * kD];
+        const int k_from = k_of(j + 1) + k_at, v_from = v_of(j) + v_at;
+        auto read_v = [&](int c) __attribute__((always_inline)) {
+          const int s = c / kD, d = c % kD;
+          const u32x2 v0 = read_transposed(lds + (v_from ^ (64 * d)) + 16 * s * kRowBytes);
+          const u32x2 v1 = read_transposed(lds + (v_from ^ (64 * d) ^ 32) + (16 * s + 8) * kRowBytes);
+          vf[c] = u32x4{v0[0], v0[1], v1[0], v1[1]};
+        };
+#pragma unroll
+        for (int c = 0; c < kS; ++c) kf[c] = *(const u32x4*)(lds + (k_from ^ (32 * c)));
+        fence();
+        float x[RT][16], sum[RT][2], at[RT];
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+          at[n] = m[n] == -INFINITY ? 0.0f : m[n];
+          sum[n][0] = sum[n][1] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            x[n][i] = fmaf(st[B][n][i], A.scale, -at[n]);
+            st[1 - B][n][i] = 0.0f;
+          }
+        }
+        fence();
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int c = 0; c < kS; ++c) {
+#pragma unroll
+          for (int n = 0; n < RT; ++n) st[1 - B][n] = mfma32<T>(kf[c], q[n][c], st[1 - B][n]);
+          fence();
+#pragma unroll
+          for (int n = 0; n < RT; ++n)
+#pragma unroll
+            for (int i = 16 * c / kS; i < 16 * (c + 1) / kS; ++i) x[n][i] = __builtin_amdgcn_exp2f(x[n][i]);
+          if (c > 0) {
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+#pragma unroll
+              for (int i = 16 * (c - 1) / kS; i < 16 * c / kS; ++i) {
+                sum[n][i & 1] += x[n][i];
+                if (i & 1) pr[n][i >> 3][(i >> 1) & 3] = Pair<T>::pack(x[n][i - 1], x[n][i]);
+              }
+          }
+#pragma unroll
+          for (int v = 2 * kD * c / kS; v < 2 * kD * (c + 1) / kS; ++v) read_v(v);
+          fence();
+        }
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+#pragma unroll
+          for (int i = 16 * (kS - 1) / kS; i < 16; ++i) {
+            sum[n][i & 1] += x[n][i];
+            if (i & 1) pr[n][i >> 3][(i >> 1) & 3] = Pair<T>::pack(x[n][i - 1], x[n][i]);
+          }
+          l[n] += sum[n][0] + sum[n][1];
+        }
+        fence();
+        __builtin_amdgcn_s_setprio(0);
+        float a[RT][2];
+#pragma unroll
+        for (int c = 0; c < 2 * kD; ++c) {
+#pragma unroll
+          for (int n = 0; n < RT; ++n) o[n][c % kD] = mfma32<T>(vf[c], pr[n][c / kD], o[n][c % kD]);
+          fence();
+          if (c >= kD) {  // the scores are there: their maxima
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+#pragma unroll
+              for (int i = 16 * (c - kD) / kD; i < 16 * (c - kD + 1) / kD; ++i)
+                a[n][i & 1] = i < 2 ? st[1 - B][n][i] : fmaxf(a[n][i & 1], st[1 - B][n][i]);
+            fence();
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < RT; ++n) {
+          const float top = fmaxf(a[n][0], a[n][1]);
+          most[n] = fmaxf(top, lane_xor<32>(top)) * A.scale;
+        }
         rescale(most);
       };
       // no way round a step's products in here: the outputs stay where they are
@@ -1001,14 +1077,12 @@ void launch_tile(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream
 
 template <typename T, int DP, int W>
 void launch_rows(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
-  if (plan.rows > 64)
+  if (plan.rows > 32)
     launch_tile<T, DP, 1, DP == 256 ? 1 : 2, DP == 256 ? 4 : 8>(a, plan, stream);
   else if (plan.rows == 16)
     launch_stream<T, DP, 1, W>(a, plan, stream);
-  else if (DP == 256 || plan.rows == 32)
+  else
     launch_stream<T, DP, 2, W>(a, plan, stream);
-  else if constexpr (DP < 256)
-    launch_stream<T, DP, 4, W>(a, plan, stream);
 }
 
 template <typename T>
@@ -1023,20 +1097,23 @@ void launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream
 
 }  // namespace
 
-// Rows of a workgroup by the rows that a sequence has on average.  A sequence of n rows has at most
+// Rows of a workgroup by the rows that a sequence has on average.  bf16, some 2000 keys: 36 rows (64 / 8 heads of 128,
+// 16 sequences) in blocks of 16, 32 and 256 take 33, 34 and 45 us, 75 rows 45 and 45 in 32 and 256, 100 rows 59 and 46;
+// 24 rows of 40 heads in 16 and 32 take 29 and 26; 75 rows of 8 heads of 256, 54 and 94 us in 32 and 128, of 16 heads of 64,
+// 31 and 41 in 32 and 256.  (64 rows a workgroup of few rows leave no registers: 51 us for the first.)  A sequence of n rows has at most
 // n group / rows + 1 blocks, and `target` / kv_heads parts at most are added over all of them; sequences
 // with several parts have at most twice their share of them.
 LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int64_t capacity, int heads, int kv_heads, int dim) {
   LbAttnPlan p;
   const int64_t group = heads / kv_heads, mean = (tokens * group + seqs - 1) / seqs;
-  p.rows = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 && dim <= 128 ? 64 : dim <= 128 ? 256 : 128;
+  p.rows = mean <= 16 ? 16 : mean <= (dim > 64 && dim <= 128 ? 80 : 112) ? 32 : dim <= 128 ? 256 : 128;
   // workgroups at once: by their LDS and registers
-  p.round = p.rows > 64 ? 256 : dim <= 64 && p.rows == 16 ? 1024 : 512;
-  p.least = p.rows > 64 ? 2048 : 256;
+  p.round = p.rows > 32 ? 256 : dim <= 64 && p.rows == 16 ? 1024 : 512;
+  p.least = p.rows > 32 ? 2048 : 256;
   // blocks of all sequences, at most, and what is shared out for so many; an empty workgroup costs a nanosecond (6000 of
   // them for one token 5 us)
   const int64_t blocks = std::min(tokens * group / p.rows + seqs, tokens * group);
-  const int64_t most = p.rows > 64 ? 512 : p.rows == 16 ? 1536 : 1024;
+  const int64_t most = p.rows > 32 ? 512 : p.rows == 16 ? 1536 : 1024;
   p.target = (int)std::min<int64_t>(most, p.round * (1 + 4 * blocks * kv_heads / p.round));
   const int64_t parts = (capacity + p.least - 1) / p.least;
   p.join = parts > 1;
