@@ -119,10 +119,12 @@ __device__ __forceinline__ int blocks_of(const Span& s, int group, int rows) { r
 __device__ __forceinline__ int parts_of(int keys, int span) { return max(1, (keys + span - 1) / span); }
 
 // The place of item `item`.  A part has the keys, in steps of STEP, that spread all sequences' keys (times their
-// blocks of rows) over the workgroups that run at once, `round` of them, and no fewer than `least`.  Parts are rounded
-// up, at most one for each block, so that `round` less the blocks is what is shared out; where blocks are many, over
-// several rounds, so that the last parts are short beside the whole.  Up to 64 sequences are read once.
-template <int STEP>
+// blocks of rows) over the workgroups that run at once, `round` of them, and no fewer than `least`; the parts of a
+// sequence are as long as each other.  Parts are rounded up, at most one for each block, so that `round` less the
+// blocks is what is shared out.  Where blocks are many: of few rows, they are shared out over several rounds, so
+// that the last parts are short beside the whole; of many rows (MANY), whose parts cost more to join, not at all,
+// and the blocks that see the most come first.  Up to 64 sequences are read once.
+template <int STEP, bool MANY>
 __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int item) {
   const int lane = threadIdx.x & 63;
   const int seqs = A.pages.seqs;
@@ -131,33 +133,55 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
     if (from + lane >= seqs) s.rows = 0;
     return s;
   };
+  // keys that a sequence's blocks take, on the mean: causal rows see half of the rows' own
+  auto keys_of = [&](const Span& s) __attribute__((always_inline)) {
+    return MANY && !A.tree ? (float)s.keys - 0.5f * (float)s.rows : (float)s.keys;
+  };
   const Span first = read(0);
   // in floating point, in one order everywhere: all workgroups get the same
   float blocks_all = (float)blocks_of(first, A.group, rows);
-  float units = (float)first.keys * blocks_all;
+  float units = keys_of(first) * blocks_all;
   for (int from = 64; from < seqs; from += 64) {
     const Span s = read(from);
     const float blocks = (float)blocks_of(s, A.group, rows);
     blocks_all += blocks;
-    units += (float)s.keys * blocks;
+    units += keys_of(s) * blocks;
   }
   blocks_all = wave_sum(blocks_all) * (float)A.kv_heads;
   const float round = (float)A.round;
-  const float share = fminf(round * (1.0f + floorf(4.0f * blocks_all / round)) - blocks_all, (float)A.target);
-  units = wave_sum(units) * (float)A.kv_heads / fmaxf(share, round * 0.5f);
-  const int want = max(A.least, units < 1e9f ? (int)units + 1 : 1 << 30);
+  const bool whole = MANY && __builtin_amdgcn_readfirstlane(blocks_all > 0.5f * round);
+  const float rounds = MANY ? 2.0f : 1.0f + floorf(4.0f * blocks_all / round);
+  const float share = fminf(fmaxf(round * rounds - blocks_all, 0.5f * round), (float)A.target);
+  units = wave_sum(units) * (float)A.kv_heads / share;
+  const int want = whole ? 1 << 30 : max(A.least, units < 1e9f ? (int)units + 1 : 1 << 30);
   Place p;
   p.seq = -1;
-  p.span = __builtin_amdgcn_readfirstlane((want + STEP - 1) / STEP * STEP);
+  const int span = __builtin_amdgcn_readfirstlane(want);
   int items = 0, slots = 0;
   for (int from = 0; from < seqs; from += 64) {
     const Span s = from ? read(from) : first;
     const int blocks = blocks_of(s, A.group, rows);
-    const int parts = parts_of(s.keys, p.span);
+    const int even = (s.keys + parts_of(s.keys, span) - 1) / parts_of(s.keys, span);
+    const int own = max((even + STEP - 1) / STEP * STEP, STEP);
+    const int parts = parts_of(s.keys, own);
     int all, all_slots;
-    const int before = items + scan64(blocks * parts, &all);
+    int before = items + scan64(blocks * parts, &all);
     const int slots_before = slots + scan64(parts > 1 ? blocks * parts : 0, &all_slots);
-    const uint64_t b = __ballot(item >= before && item < before + blocks * parts);
+    uint64_t b = __ballot(item >= before && item < before + blocks * parts);
+    if (MANY && whole && seqs <= 64 && item < all) {
+      // by the blocks' place in their sequence, the last ones of the longest first
+      int left = item, level = __builtin_amdgcn_readfirstlane((int)wave_max((float)blocks));
+      uint64_t at;
+      do {
+        --level;
+        at = __ballot(blocks > level);
+        left -= __builtin_popcountll(at);
+      } while (left >= 0);
+      left += __builtin_popcountll(at);
+      const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(at >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)at, 0));
+      b = __ballot(blocks > level && rank == left);
+      before = item - (blocks - 1 - level);
+    }
     if (b) {
       const int l = __builtin_ctzll(b);
       p.seq = from + l;
@@ -167,6 +191,7 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
       p.s.base = __builtin_amdgcn_readlane(s.base, l);
       p.blocks = __builtin_amdgcn_readlane(blocks, l);
       p.parts = __builtin_amdgcn_readlane(parts, l);
+      p.span = __builtin_amdgcn_readlane(own, l);
       p.local = item - __builtin_amdgcn_readlane(before, l);
       p.slot = __builtin_amdgcn_readlane(slots_before, l) + p.local;
       return p;
@@ -261,8 +286,12 @@ __device__ __forceinline__ int swizzle(int row) {
 // 16 bytes a lane from base + offset to LDS, 1 KB from `lds` on.  In assembly, so that the compiler does not wait for it
 // before reads of other stages; the kernels wait themselves.  Nothing is loaded into registers.
 __device__ __forceinline__ void load_to_lds(uint32_t lds, const void* base, uint32_t offset) {
+  // scalars, whatever the compiler knows of them
+  const uint64_t p = (uint64_t)(uintptr_t)base;
+  const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)p), high = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+  const uint64_t from = (uint64_t)high << 32 | low;  // (the builtin's int, or'ed as it is, would spread its sign)
   __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane(lds)),
-                   "v"(offset), "s"(base)
+                   "v"(offset), "s"(from)
                    : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
@@ -326,7 +355,7 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
   const int w = wave_id(), lane = threadIdx.x & 63;
   const int r16 = lane & 15, g = lane >> 4;
   const int kv_head = blockIdx.x % A.kv_heads;
-  const Place p = place_of<32 * W>(A, kRows, blockIdx.x / A.kv_heads);
+  const Place p = place_of<32 * W, false>(A, kRows, blockIdx.x / A.kv_heads);
   if (p.seq < 0) return;  // the whole workgroup: all waves computed the same
   // causal rows: the last block, which sees the most, first
   const int block = p.blocks - 1 - p.local / p.parts, part = p.local % p.parts;
@@ -595,7 +624,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   const int w = wave_id(), lane = threadIdx.x & 63;
   const int r32 = lane & 31, h = lane >> 5;
   const int kv_head = blockIdx.x % A.kv_heads;
-  const Place p = place_of<kKeys>(A, kRows, blockIdx.x / A.kv_heads);
+  const Place p = place_of<kKeys, true>(A, kRows, blockIdx.x / A.kv_heads);
   if (p.seq < 0) return;  // the whole workgroup: all waves computed the same
   // causal rows: the last block, which sees the most, first
   const int block = p.blocks - 1 - p.local / p.parts, part = p.local % p.parts;
@@ -644,10 +673,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   const int mask = (1 << P.shift) - 1;
   auto page_at = [&](int key) __attribute__((always_inline)) { return table[min(key >> P.shift, P.columns - 1)]; };
   auto is_page = [&](int page) __attribute__((always_inline)) { return (uint32_t)page < (uint32_t)P.pages; };
-  // whether every key has a page: most steps do not ask again
-  bool some = false;
-  for (int c = (from >> P.shift) + lane; c <= (to - 1) >> P.shift; c += 64) some = some || !is_page(P.table[p.seq * P.table_stride + c]);
-  const bool good = __ballot(some) == 0;
+  bool good = true;  // every key has a page
   // this wave's part of tile t's keys and values into their stages
   const int load_row = lane / kPieces, load_piece = lane % kPieces;
   auto fill = [&](int t) __attribute__((always_inline)) {
@@ -797,6 +823,9 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
 
   if (tiles > 0) {
     fill(0);
+    // most steps do not ask again whether their keys have a page
+    for (int c = (from >> P.shift) + lane; c <= (to - 1) >> P.shift; c += 64) good = good && is_page(P.table[p.seq * P.table_stride + c]);
+    good = __ballot(!good) == 0;
     const int clear = good ? min(steps, (min(own.full, to) - from) >> 5) : 0;  // steps that all rows see whole
     meet(0);
     if (tiles > 1) fill(1);
@@ -1109,12 +1138,12 @@ LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int64_t capacity, int heads, i
   p.rows = mean <= 16 ? 16 : mean <= (dim > 64 && dim <= 128 ? 80 : 112) ? 32 : dim <= 128 ? 256 : 128;
   // workgroups at once: by their LDS and registers
   p.round = p.rows > 32 ? 256 : dim <= 64 && p.rows == 16 ? 1024 : 512;
-  p.least = p.rows > 32 ? 2048 : 256;
+  p.least = p.rows > 32 ? 1024 : 256;
   // blocks of all sequences, at most, and what is shared out for so many; an empty workgroup costs a nanosecond (6000 of
   // them for one token 5 us)
   const int64_t blocks = std::min(tokens * group / p.rows + seqs, tokens * group);
   const int64_t most = p.rows > 32 ? 512 : p.rows == 16 ? 1536 : 1024;
-  p.target = (int)std::min<int64_t>(most, p.round * (1 + 4 * blocks * kv_heads / p.round));
+  p.target = p.rows > 32 ? (int)most : (int)std::min<int64_t>(most, p.round * (1 + 4 * blocks * kv_heads / p.round));
   const int64_t parts = (capacity + p.least - 1) / p.least;
   p.join = parts > 1;
   const int64_t share = (p.target + kv_heads - 1) / kv_heads + 1;
