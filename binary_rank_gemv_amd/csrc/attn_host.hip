@@ -32,7 +32,8 @@ inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 constexpr int64_t kMaxTokens = 1 << 21;
 constexpr int kMaxHeads = 1 << 10;
 constexpr int64_t kMaxStride = 1ll << 40;
-constexpr int64_t kMaxGroups = 1 << 23;  // workgroups of 256 threads: a grid holds fewer than 2^32
+constexpr int64_t kMaxGroups = 1 << 22;  // workgroups of 512 threads: a grid holds fewer than 2^32
+constexpr int64_t kMaxRows = 1 << 30;
 
 #define LB_TRY(expr)                   \
   do {                                 \
@@ -336,7 +337,7 @@ lb_status littlebit_cache_attention_fwd(const lb_cache* cache, const lb_cache_ba
   if (tokens == 0) return LB_OK;
   if (q->p == out->p) return fail(LB_ERR_INVALID_ARG, "%s: out must not be q", name);
   const LbAttnPlan plan = lb_attn_plan(tokens, batch->seqs, (int64_t)batch->columns * cache->page_size, q->heads, cache->heads, cache->dim);
-  if (plan.grid > kMaxGroups || tokens * q->heads > 4 * kMaxGroups)
+  if (plan.grid > kMaxGroups || tokens * q->heads > kMaxRows)
     return fail(LB_ERR_UNSUPPORTED, "%s: %lld tokens of %d heads are too many for one call", name, (long long)tokens, q->heads);
   const size_t need = lb_attn_workspace(plan, tokens, q->heads, cache->heads, cache->dim);
   if (need > 0 && (!ws || !aligned(ws, 16)))

@@ -503,8 +503,10 @@ void launch_bwd(const LbRopeBwdArgs& a, hipStream_t stream) {
 }
 
 // ------------------------------------------------------------------ accepted rows
-// A workgroup: the accepted rows of one head's keys or values, all in registers before the
-// first is written.  64 rows of 256 channels at most: eight 16-byte pieces a thread.
+// A workgroup: the accepted rows of one head's keys or values, all in registers before the first is written: at
+// most PIECES 16-byte pieces a thread, eight for 64 rows of 256 channels.  Latency bounds it, and, of many
+// sequences, how many workgroups run at once: 48 trees, 40 heads of 128, 9 rows each, 9.7 us with room for 8 pieces, 4.4 with one.
+template <int PIECES>
 __global__ __launch_bounds__(256) void lb_accept_kernel(const LbPages P, int dim, const int32_t* __restrict__ path,
                                                         int columns) {
   const int seq = blockIdx.y, head = blockIdx.x >> 1;
@@ -517,12 +519,12 @@ __global__ __launch_bounds__(256) void lb_accept_kernel(const LbPages P, int dim
     const int page = row >= 0 && row < s.rows && key < s.keys ? page_of(P, seq, key) : -1;
     return page < 0 ? -1l : page * P.page + (key & ((1 << P.shift) - 1)) * P.slot;
   };
-  u32x4 r[8];
-  long to[8];
+  u32x4 r[PIECES];
+  long to[PIECES];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int item = threadIdx.x + 256 * i;
-    const int j = item / pieces, c = item - j * pieces;
+  for (int i = 0; i < PIECES; ++i) {
+    const uint32_t item = threadIdx.x + 256 * i;
+    const int j = item / (uint32_t)pieces, c = item - j * pieces;
     to[i] = -1;
     r[i] = u32x4{0, 0, 0, 0};
     if (j < columns) {
@@ -537,10 +539,10 @@ __global__ __launch_bounds__(256) void lb_accept_kernel(const LbPages P, int dim
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) __asm__ volatile("" : "+v"(r[i]));  // a use: every load of this wave has come back
+  for (int i = 0; i < PIECES; ++i) __asm__ volatile("" : "+v"(r[i]));  // a use: every load of this wave has come back
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < PIECES; ++i)
     if (to[i] >= 0) *(u32x4*)(cache + to[i]) = r[i];
 }
 
@@ -581,6 +583,13 @@ hipError_t lb_launch_rope_bwd(const LbRopeBwdArgs& a, int dtype, hipStream_t str
 }
 
 hipError_t lb_launch_accept(const LbPages& p, int heads, int dim, const int32_t* path, int columns, hipStream_t stream) {
-  hipLaunchKernelGGL(lb_accept_kernel, dim3(2 * heads, p.seqs), dim3(256), 0, stream, p, dim, path, columns);
+  const dim3 grid(2 * heads, p.seqs);
+  const int items = columns * (dim / 8);
+  if (items <= 256)
+    hipLaunchKernelGGL(lb_accept_kernel<1>, grid, dim3(256), 0, stream, p, dim, path, columns);
+  else if (items <= 512)
+    hipLaunchKernelGGL(lb_accept_kernel<2>, grid, dim3(256), 0, stream, p, dim, path, columns);
+  else
+    hipLaunchKernelGGL(lb_accept_kernel<8>, grid, dim3(256), 0, stream, p, dim, path, columns);
   return hipGetLastError();
 }

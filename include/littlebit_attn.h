@@ -65,6 +65,7 @@ typedef struct {
  * Angles are formed in 64 bits and their turns taken off there, so far positions
  * keep their digits; everything else is in fp32, rounded to the type once.
  * Values of any size are normed, those whose squares fp32 does not hold (bf16) too.
+ * A head of zeros needs eps > 0.
  */
 typedef struct {
   const int32_t *positions;
@@ -168,7 +169,9 @@ lb_status littlebit_cache_append(const lb_cache *cache, const lb_cache_batch *ba
  *   ws         littlebit_cache_attention_workspace_bytes(...) bytes (may be 0, then ws may be
  *              NULL), 16-byte aligned.
  * Scores, softmax and sums are in fp32; the probabilities are rounded to the cache's type for
- * their product with the values.  The same call gives the same bits.
+ * their product with the values (the matrix units take both in one type), relative to a maximum
+ * that is at most 2^8 behind, so that they keep the type's digits.  The same call gives the same bits.
+ * tokens x q->heads <= 2^30, fewer where the grid holds no more.
  */
 size_t littlebit_cache_attention_workspace_bytes(const lb_cache *cache, const lb_cache_batch *batch,
                                                  int64_t tokens, int32_t heads);
@@ -182,7 +185,8 @@ lb_status littlebit_cache_attention_fwd(const lb_cache *cache, const lb_cache_ba
  * After a tree is verified: the keys and values of its accepted rows moved together.
  * For every sequence and j < columns with path[i][j] >= 0, the keys and values of the
  * sequence's row path[i][j] are copied to where those of its row j lie; all are read before
- * any is written.  With `lens` lowered to the keys before the rows plus the accepted ones,
+ * any is written (of one sequence: two sequences of a call must not share pages that hold
+ * their rows).  With `lens` lowered to the keys before the rows plus the accepted ones,
  * the cache is that of a text which had the accepted tokens only.
  *   path       int32 [seqs][columns], contiguous; negative entries, and those that name no
  *              row of the sequence, move nothing.  1 <= columns <= LB_TREE_MAX.

@@ -282,7 +282,7 @@ def check_attention(got, lse, q, p, scale, tree=None):
         g = f64(lse)
         assert (np.isneginf(g[mine]) == np.isneginf(want_lse[mine])).all()
         fine = mine & np.isfinite(want_lse)
-        assert (np.abs(g - want_lse)[fine] <= (ds + 4 * U * (1 + np.abs(want_lse)))[fine]).all()
+        assert (np.abs(g[fine] - want_lse[fine]) <= (ds + 4 * U * (1 + np.abs(want_lse)))[fine]).all()
 
 
 def run_attention(attn, p, q, scale=None, tree=None, how="own"):
@@ -304,7 +304,8 @@ ATTEND = [
     ([(7, 900), (16, 3), (1, 2000)], 16, 2, 128, 128), ([(5, 0), (33, 7)], 6, 2, 64, 16), ([(70, 200)], 7, 1, 128, 64),
     ([(150, 0), (0, 0), (3, 50)], 4, 4, 192, 8), ([(40, 333)], 4, 2, 256, 32), ([(1, 5000)], 2, 1, 128, 64),
     ([(9, 4000), (1, 1)], 4, 1, 256, 64), ([(3, 2500)], 2, 2, 64, 8), ([(300, 40)], 3, 1, 64, 16), ([(1, 3000)], 40, 1, 24, 16),
-    ([(130, 1111), (257, 0)], 4, 2, 128, 16),
+    ([(130, 1111), (257, 0)], 4, 2, 128, 16), ([(1, 700), (2, 90)], 64, 1, 128, 1024), ([(100, 6000)], 4, 1, 128, 64),
+    ([(40, 2500), (41, 2400)], 16, 4, 64, 32), ([(200, 1500)], 1, 1, 256, 128), ([(90, 40), (300, 7), (513, 0), (1, 9)], 2, 2, 96, 8),
 ]
 
 
@@ -327,7 +328,7 @@ def tree_words(rng, rows):
 
 
 TREES = [([(1, 0)], 1, 1, 64, 8), ([(2, 0), (16, 31)], 4, 4, 128, 16), ([(64, 0)], 2, 1, 128, 8), ([(64, 1000), (13, 64), (0, 4), (27, 1)], 8, 2, 128, 64),
-         ([(33, 4099)], 4, 1, 64, 32), ([(61, 77), (5, 3)], 3, 1, 256, 16), ([(16, 2000)], 2, 2, 80, 64), ([(64, 31), (64, 32), (64, 33)], 8, 8, 96, 8)]
+         ([(33, 4099)], 4, 1, 64, 32), ([(61, 77), (5, 3)], 3, 1, 256, 16), ([(16, 2000)], 2, 2, 80, 64), ([(64, 31), (64, 32), (64, 33)], 8, 8, 96, 8), ([(64, 5000)], 4, 1, 128, 64), ([(50, 3000), (64, 9)], 8, 2, 256, 16)]
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
@@ -430,19 +431,22 @@ def test_what_is_not_seen_has_no_part(attn, rows, value, dt):
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
-def test_values_that_are_seen_keep_their_infinities(attn, dt):
-    """Infinite values of one sign in a channel give that infinity to the rows that see them, of both signs NaN."""
-    p = Paged(attn, 8, [(6, 40)], 1, 128, 8, TYPES[dt])
+@pytest.mark.parametrize("rows,cached,heads,dim", [(6, 40, 2, 128), (300, 40, 1, 128), (200, 2000, 2, 64), (150, 1030, 1, 256), (40, 900, 2, 256)])
+def test_values_that_are_seen_keep_their_infinities(attn, rows, cached, heads, dim, dt):
+    """Infinite values of one sign in a channel give that infinity to the rows that see them, of both signs NaN; among
+    the keys before the rows they reach every row."""
+    p = Paged(attn, 8, [(rows, cached)], 1, dim, 8, TYPES[dt])
     at = lambda key: oa.place(0, key, p.table, 8, p.cache.k.shape[0])  # noqa: E731
-    for key, channel, value in ((41, 3, float("inf")), (43, 3, -float("inf")), (44, 100, -float("inf")), (42, 50, float("nan"))):
-        p.cache.v[at(key)[0], :, at(key)[1], channel] = value
-    out, _ = run_attention(attn, p, randn(9, 6, 2, 128).to(p.t))
+    inf, mid = float("inf"), rows // 2
+    for row, channel, value in ((1, 3, inf), (3, 3, -inf), (4, dim - 28, -inf), (mid, 30, float("nan")), (2 - cached, 9, inf)):
+        p.cache.v[at(cached + row)[0], :, at(cached + row)[1], channel] = value
+    out, _ = run_attention(attn, p, randn(9, rows, heads, dim).to(p.t))
     o = out.float()
-    assert torch.isfinite(o[0]).all()
-    assert (o[1:3, :, 3] == float("inf")).all() and torch.isnan(o[3:, :, 3]).all()
-    assert (o[4:, :, 100] == -float("inf")).all() and torch.isfinite(o[:4, :, 100]).all()
-    assert torch.isnan(o[2:, :, 50]).all() and torch.isfinite(o[:2, :, 50]).all()
-    rest = [d for d in range(128) if d not in (3, 50, 100)]
+    assert (o[:, :, 9] == inf).all() and torch.isfinite(o[0, :, [3, 30]]).all()
+    assert (o[1:3, :, 3] == inf).all() and torch.isnan(o[3:, :, 3]).all()
+    assert (o[4:, :, dim - 28] == -inf).all() and torch.isfinite(o[:4, :, dim - 28]).all()
+    assert torch.isnan(o[mid:, :, 30]).all() and torch.isfinite(o[:mid, :, 30]).all()
+    rest = [d for d in range(dim) if d not in (3, 9, 30, dim - 28)]
     assert torch.isfinite(o[:, :, rest]).all()
 
 
