@@ -10,8 +10,8 @@
 // for is free as long as both operands agree.  V^T is read from LDS through the transposing
 // read.
 //
-// Work is spread by the keys that there are: span_of all sequences gives the keys a workgroup takes, so
-// that about `target` workgroups share them, whatever the lengths; a sequence's parts
+// Work is spread by the keys that there are: every workgroup adds up all sequences' keys and takes as many as
+// leave its share to each of those that run at once, whatever the lengths; a sequence's parts
 // are joined by a second kernel.  All of that is computed on the device, so that a captured call
 // serves any lengths.
 #include <algorithm>
@@ -30,6 +30,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kPartKeys = 512;  // what beginning, writing and joining a part of many rows costs, in keys
 constexpr float kSlack = 8.0f;  // log2: how far a maximum may grow before the sums are scaled down
 
 template <typename T>
@@ -123,7 +124,9 @@ __device__ __forceinline__ int parts_of(int keys, int span) { return max(1, (key
 // sequence are as long as each other.  Parts are rounded up, at most one for each block, so that `round` less the
 // blocks is what is shared out.  Where blocks are many: of few rows, they are shared out over several rounds, so
 // that the last parts are short beside the whole; of many rows (MANY), whose parts cost more to join, not at all,
-// and the blocks that see the most come first.  Up to 64 sequences are read once.
+// and the blocks that see the most come first.  Where blocks of many rows are few, lengths of parts are compared by the
+// rounds they take (2 sequences of 64 rows over 16000 keys of 64 / 8 heads of 128: 92 -> 71 us, 500 tokens on 4000 of 16 / 4
+// heads of 256 104 -> 73; 3 of 200 over 20000 of 32 / 8 heads, though, 213 -> 221).  Up to 64 sequences are read once.
 template <int STEP, bool MANY>
 __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int item) {
   const int lane = threadIdx.x & 63;
@@ -156,7 +159,25 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
   const int want = whole ? 1 << 30 : max(A.least, units < 1e9f ? (int)units + 1 : 1 << 30);
   Place p;
   p.seq = -1;
-  const int span = __builtin_amdgcn_readfirstlane(want);
+  int span = __builtin_amdgcn_readfirstlane(want);
+  if (MANY && !whole && seqs <= 64) {
+    // a lane each: the longest sequence in lane + 1 parts, and the others in parts of that length
+    const int longest = __builtin_amdgcn_readfirstlane((int)wave_max(first.rows > 0 ? (float)first.keys : 0.0f));
+    const int even = (longest / (lane + 1) + STEP) / STEP * STEP, mine = lane ? even : 1 << 30;
+    const int own_blocks = blocks_of(first, A.group, rows);
+    int all = 0, joined = 0;
+    for (uint64_t left = __ballot(own_blocks > 0); left; left &= left - 1) {
+      const int l = __builtin_ctzll(left);
+      const int b = __builtin_amdgcn_readlane(own_blocks, l), parts = parts_of(__builtin_amdgcn_readlane(first.keys, l), mine);
+      all += b * parts;
+      joined += parts > 1 ? b * parts : 0;
+    }
+    const bool fits = all <= (int)(gridDim.x / A.kv_heads) && joined <= A.slots;
+    const float rounds = ceilf((float)all * (float)A.kv_heads / round);
+    const float cost = lane == 0 || fits ? rounds * (float)(even + kPartKeys) : INFINITY;
+    const uint64_t best = __ballot(cost == -wave_max(-cost));
+    span = __builtin_amdgcn_readlane(mine, __builtin_ctzll(best | 1ull << 63));
+  }
   int items = 0, slots = 0;
   for (int from = 0; from < seqs; from += 64) {
     const Span s = from ? read(from) : first;
@@ -341,8 +362,9 @@ __device__ __forceinline__ f32x4 odd_values(const char* p, int d, int dim, bool 
 // 16 NT rows a workgroup; its W waves have the same rows and take turns at steps of 32 keys, each
 // with its own stages in LDS, filled by direct loads: the next step's keys are under way
 // from the products with this one's on, its values from their products on.  No wave waits for another until the
-// end, when the waves' sums are joined in LDS.  Bytes bound it.
-//
+// end, when the waves' sums are joined in LDS.  Bytes bound it: 32 sequences of one
+// token over 1 to 8000 keys of 64 / 8 heads of 128, bf16, 113 us, 5.2 TB/s (a large copy reaches 5.1); one over 4000 keys of
+// 40 heads, fp16, 14 to 17 us, of which some 5 are the way to the first keys.
 template <typename T, int DP, int NT, int W>
 __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream_kernel(const LbAttnArgs A) {
   constexpr int kRowBytes = 2 * DP, kPieces = DP / 8, kStage = 32 * kRowBytes;
@@ -597,14 +619,19 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
 }
 
 // ----------------------------------------------------------------------- many rows
-// A workgroup of four waves has 128 RT rows of a sequence and key head, each wave 32 RT of them as the columns of 32 x 32
+// A workgroup of W waves has 32 W rows of a sequence and key head, each wave 32 of them as the columns of 32 x 32
 // matrix steps, and all its keys in tiles of KT x 32, which the waves load into LDS together and all read.  The products
 // bound it, and the exponentials beside them: a wave's instructions are laid out so that the two run side by side.
 // While step j's scores become probabilities, the products of step j + 1's keys are formed; while the maxima of
-// step j + 1 are taken, those of step j's values.  Every operand that is read from LDS serves RT products.
+// step j + 1 are taken, those of step j's values.
 //
 // Keys have two stages, values three: a tile's values are read until one step after its keys.  One barrier a tile,
 // where the next tile has landed; the one after it is then asked for.
+//
+// bf16, 64 / 8 heads of 128: a prompt of 4000 tokens over 4100 cached ones 810 us, 0.99 PFLOP/s (1.04 for 16384 tokens of
+// 32 / 8), where a large library product runs at 1.23 and a loop of this kernel's instructions alone, without barriers, at
+// 1.32.  Slower were halves of the waves a step apart (916 us), tiles asked for two ahead (833), and the compiler's own
+// order of a step (850 to 870).
 template <typename T>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (__is_same(T, f16))
@@ -613,12 +640,12 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
 }
 
-template <typename T, int DP, int RT, int KT, int W>
-__global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A) {
+template <typename T, int DP, int KT, int W>
+__global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void lb_attn_tile_kernel(const LbAttnArgs A) {
   constexpr int kRowBytes = 2 * DP, kPieces = DP / 8, kKeys = 32 * KT, kStage = kKeys * kRowBytes;
   constexpr int kPer = 1024 / kRowBytes;       // keys of one load of a wave
   constexpr int kLoads = kStage / 1024 / W;    // loads of a wave for a tile's keys, and for its values
-  constexpr int kRows = 32 * RT * W, kS = DP / 16, kD = DP / 32;
+  constexpr int kRows = 32 * W, kS = DP / 16, kD = DP / 32;
   static_assert(kPer <= 8 && kLoads * 1024 * W == kStage, "a load lies in one page");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[5 * kStage];
   const int w = wave_id(), lane = threadIdx.x & 63;
@@ -633,10 +660,10 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   const int parts = parts_of(sight.most, p.span);
   if (part >= parts || (parts > 1 && p.slot >= A.slots)) return;  // the latter: starts that name rows twice
   const int from = part * p.span, to = min(from + p.span, sight.most);
-  const int first_row = block * kRows + 32 * RT * w;
+  const int first_row = block * kRows + 32 * w;
   // this wave's own rows: their keys end earlier, and may be seen by all of them later
   const bool has_rows = first_row < all_rows;
-  const Sight own = sight_of(A, p.s, first_row, 32 * RT);
+  const Sight own = sight_of(A, p.s, first_row, 32);
   const int steps = has_rows ? (max(min(own.most, to) - from, 0) + 31) / 32 : 0;
   const int tiles = (max(to - from, 0) + kKeys - 1) / kKeys;
 
@@ -649,24 +676,19 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
     __syncthreads();
   }
 
-  // queries, operands of S^T = K Q^T: row r32 of a tile, channels 16 s + 8 h + (0..7)
-  u32x4 q[RT][kS];
-  int sees[RT];
-  uint64_t word[RT];
+  // the row's query, operand of S^T = K Q^T: channels 16 s + 8 h + (0..7)
+  u32x4 q[kS];
+  const int row = first_row + r32;
+  const bool in = row < all_rows;
+  const int t = in ? (uint32_t)row / (uint32_t)A.group : 0, head = kv_head * A.group + (in ? row - t * A.group : 0);
+  const T* src = (const T*)A.q + (p.s.start + t) * A.qt + head * A.qh;
 #pragma unroll
-  for (int n = 0; n < RT; ++n) {
-    const int row = first_row + 32 * n + r32;
-    const bool in = row < all_rows;
-    const int t = in ? (uint32_t)row / (uint32_t)A.group : 0, head = kv_head * A.group + (in ? row - t * A.group : 0);
-    const T* src = (const T*)A.q + (p.s.start + t) * A.qt + head * A.qh;
-#pragma unroll
-    for (int s = 0; s < kS; ++s) {
-      const int d = 16 * s + 8 * h;
-      q[n][s] = in && d < A.dim ? with_sign(A, load_any<u32x4>(src + d)) : u32x4{0, 0, 0, 0};
-    }
-    word[n] = A.tree && in ? (uint64_t)A.tree[p.s.start + t] : 0;
-    sees[n] = in ? A.tree ? sight.most : min(sight.most, p.s.base + t + 1) : 0;
+  for (int s = 0; s < kS; ++s) {
+    const int d = 16 * s + 8 * h;
+    q[s] = in && d < A.dim ? with_sign(A, load_any<u32x4>(src + d)) : u32x4{0, 0, 0, 0};
   }
+  const uint64_t word = A.tree && in ? (uint64_t)A.tree[p.s.start + t] : 0;
+  const int sees = in ? A.tree ? sight.most : min(sight.most, p.s.base + t + 1) : 0;
 
   typedef const __attribute__((address_space(4))) int32_t* Table;
   const Table table = (Table)(uintptr_t)(P.table + p.seq * P.table_stride);
@@ -711,9 +733,9 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
     __asm__ volatile("" ::: "memory");
   };
 
-  // which of a step's keys row n sees
-  auto seen = [&](int n, int key, uint32_t there) __attribute__((always_inline)) {
-    return seen_of(A, p.s.base, key, there, sees[n], word[n]);
+  // which of a step's keys the row sees
+  auto seen = [&](int key, uint32_t there) __attribute__((always_inline)) {
+    return seen_of(A, p.s.base, key, there, sees, word);
   };
   // keys of a step that have a page, a bit each
   auto paged = [&](int key) __attribute__((always_inline)) {
@@ -723,19 +745,14 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
     return v;
   };
 
-  f32x16 st[2][RT], o[RT][kD];
-  u32x4 pr[RT][2];
-  float m[RT], l[RT];
+  f32x16 st[2], o[kD];
+  u32x4 pr[2];
+  float m = -INFINITY, l = 0.0f;
+  pr[0] = pr[1] = u32x4{0, 0, 0, 0};
 #pragma unroll
-  for (int n = 0; n < RT; ++n) {
-    m[n] = -INFINITY;
-    l[n] = 0.0f;
-    pr[n][0] = pr[n][1] = u32x4{0, 0, 0, 0};
+  for (int d = 0; d < kD; ++d)
 #pragma unroll
-    for (int d = 0; d < kD; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[n][d][i] = 0.0f;
-  }
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   const int k_at = r32 * kRowBytes + 16 * (h ^ swizzle<DP>(r32));
   const int v_row = 4 * h + ((lane & 15) >> 2);
   const int v_at = v_row * kRowBytes + 16 * ((2 * (lane >> 4 & 1) + ((lane & 3) >> 1)) ^ swizzle<DP>(v_row)) + 8 * (lane & 1);
@@ -743,17 +760,14 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
   auto k_of = [&](int j) __attribute__((always_inline)) { return (j / KT & 1) * kStage + j % KT * 32 * kRowBytes; };
   auto v_of = [&](int j) __attribute__((always_inline)) { return (2 + j / KT % 3) * kStage + j % KT * 32 * kRowBytes; };
 
-  auto scores = [&](int j, f32x16 (&s)[RT]) __attribute__((always_inline)) {
+  auto scores = [&](int j, f32x16& s) __attribute__((always_inline)) {
     const int at = k_of(j) + k_at;
 #pragma unroll
-    for (int n = 0; n < RT; ++n)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
+    for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
     for (int c = 0; c < kS; ++c) {
       const u32x4 k = *(const u32x4*)(lds + (at ^ (32 * c)));
-#pragma unroll
-      for (int n = 0; n < RT; ++n) s[n] = mfma32<T>(k, q[n][c], s[n]);
+      s = mfma32<T>(k, q[c], s);
     }
   };
   auto products = [&](int j) __attribute__((always_inline)) {
@@ -765,52 +779,42 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
         const u32x2 v0 = read_transposed(lds + (at ^ (64 * d)) + 16 * s * kRowBytes);
         const u32x2 v1 = read_transposed(lds + (at ^ (64 * d) ^ 32) + (16 * s + 8) * kRowBytes);
         const u32x4 v = {v0[0], v0[1], v1[0], v1[1]};
-#pragma unroll
-        for (int n = 0; n < RT; ++n) o[n][d] = mfma32<T>(v, pr[n][s], o[n][d]);
+        o[d] = mfma32<T>(v, pr[s], o[d]);
       }
     }
   };
-  // the largest score of each row so far
-  auto maxima = [&](const f32x16 (&s)[RT], float (&most)[RT]) __attribute__((always_inline)) {
+  // the row's largest score
+  auto maximum = [&](const f32x16& s) __attribute__((always_inline)) {
+    float a = s[0], b = s[1];
 #pragma unroll
-    for (int n = 0; n < RT; ++n) {
-      float a = s[n][0], b = s[n][1];
+    for (int i = 2; i < 16; i += 2) {
+      a = fmaxf(a, s[i]);
+      b = fmaxf(b, s[i + 1]);
+    }
+    a = fmaxf(a, b);
+    return fmaxf(a, lane_xor<32>(a)) * A.scale;
+  };
+  auto rescale = [&](float most) __attribute__((always_inline)) {
+    if (__ballot(most > m + kSlack)) {
+      const float up = fmaxf(m, most);
+      const float a = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - up);
+      m = up;
+      l *= a;
 #pragma unroll
-      for (int i = 2; i < 16; i += 2) {
-        a = fmaxf(a, s[n][i]);
-        b = fmaxf(b, s[n][i + 1]);
-      }
-      a = fmaxf(a, b);
-      most[n] = fmaxf(a, lane_xor<32>(a)) * A.scale;
+      for (int d = 0; d < kD; ++d) o[d] *= a;
     }
   };
-  auto rescale = [&](const float (&most)[RT]) __attribute__((always_inline)) {
+  auto probabilities = [&](const f32x16& s) __attribute__((always_inline)) {
+    const float at = m == -INFINITY ? 0.0f : m;
+    float x[16], sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int n = 0; n < RT; ++n) {
-      if (__ballot(most[n] > m[n] + kSlack)) {
-        const float up = fmaxf(m[n], most[n]);
-        const float a = m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[n] - up);
-        m[n] = up;
-        l[n] *= a;
-#pragma unroll
-        for (int d = 0; d < kD; ++d) o[n][d] *= a;
-      }
+    for (int i = 0; i < 16; ++i) {
+      x[i] = __builtin_amdgcn_exp2f(fmaf(s[i], A.scale, -at));
+      sum[i & 1] += x[i];
     }
-  };
-  auto probabilities = [&](const f32x16 (&s)[RT]) __attribute__((always_inline)) {
+    l += sum[0] + sum[1];
 #pragma unroll
-    for (int n = 0; n < RT; ++n) {
-      const float at = m[n] == -INFINITY ? 0.0f : m[n];
-      float x[16], sum[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        x[i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], A.scale, -at));
-        sum[i & 1] += x[i];
-      }
-      l[n] += sum[0] + sum[1];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) pr[n][i >> 2][i & 3] = Pair<T>::pack(x[2 * i], x[2 * i + 1]);
-    }
+    for (int i = 0; i < 8; ++i) pr[i >> 2][i & 3] = Pair<T>::pack(x[2 * i], x[2 * i + 1]);
   };
   // before step j is left: where the next one begins a tile, that has landed in all waves, and the one after it is asked for
   auto advance = [&](int j) __attribute__((always_inline)) {
@@ -829,12 +833,10 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
     const int clear = good ? min(steps, (min(own.full, to) - from) >> 5) : 0;  // steps that all rows see whole
     meet(0);
     if (tiles > 1) fill(1);
-    float most[RT];
     int j = 0;
     if (clear > 0) {
       scores(0, st[0]);
-      maxima(st[0], most);
-      rescale(most);
+      rescale(maximum(st[0]));
       // A step's instructions in the order they are wanted: reads well ahead of their products, and between the products
       // the exponentials and the maxima.  Nothing is moved across a fence.
       auto fence = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
@@ -852,73 +854,54 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
 #pragma unroll
         for (int c = 0; c < kS; ++c) kf[c] = *(const u32x4*)(lds + (k_from ^ (32 * c)));
         fence();
-        float x[RT][16], sum[RT][2], at[RT];
+        const float at = m == -INFINITY ? 0.0f : m;
+        float x[16], sum[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int n = 0; n < RT; ++n) {
-          at[n] = m[n] == -INFINITY ? 0.0f : m[n];
-          sum[n][0] = sum[n][1] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[n][i] = fmaf(st[B][n][i], A.scale, -at[n]);
-            st[1 - B][n][i] = 0.0f;
-          }
+        for (int i = 0; i < 16; ++i) {
+          x[i] = fmaf(st[B][i], A.scale, -at);
+          st[1 - B][i] = 0.0f;
         }
         fence();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int c = 0; c < kS; ++c) {
-#pragma unroll
-          for (int n = 0; n < RT; ++n) st[1 - B][n] = mfma32<T>(kf[c], q[n][c], st[1 - B][n]);
+          st[1 - B] = mfma32<T>(kf[c], q[c], st[1 - B]);
           fence();
 #pragma unroll
-          for (int n = 0; n < RT; ++n)
-#pragma unroll
-            for (int i = 16 * c / kS; i < 16 * (c + 1) / kS; ++i) x[n][i] = __builtin_amdgcn_exp2f(x[n][i]);
+          for (int i = 16 * c / kS; i < 16 * (c + 1) / kS; ++i) x[i] = __builtin_amdgcn_exp2f(x[i]);
           if (c > 0) {
 #pragma unroll
-            for (int n = 0; n < RT; ++n)
-#pragma unroll
-              for (int i = 16 * (c - 1) / kS; i < 16 * c / kS; ++i) {
-                sum[n][i & 1] += x[n][i];
-                if (i & 1) pr[n][i >> 3][(i >> 1) & 3] = Pair<T>::pack(x[n][i - 1], x[n][i]);
-              }
+            for (int i = 16 * (c - 1) / kS; i < 16 * c / kS; ++i) {
+              sum[i & 1] += x[i];
+              if (i & 1) pr[i >> 3][(i >> 1) & 3] = Pair<T>::pack(x[i - 1], x[i]);
+            }
           }
 #pragma unroll
           for (int v = 2 * kD * c / kS; v < 2 * kD * (c + 1) / kS; ++v) read_v(v);
           fence();
         }
 #pragma unroll
-        for (int n = 0; n < RT; ++n) {
-#pragma unroll
-          for (int i = 16 * (kS - 1) / kS; i < 16; ++i) {
-            sum[n][i & 1] += x[n][i];
-            if (i & 1) pr[n][i >> 3][(i >> 1) & 3] = Pair<T>::pack(x[n][i - 1], x[n][i]);
-          }
-          l[n] += sum[n][0] + sum[n][1];
+        for (int i = 16 * (kS - 1) / kS; i < 16; ++i) {
+          sum[i & 1] += x[i];
+          if (i & 1) pr[i >> 3][(i >> 1) & 3] = Pair<T>::pack(x[i - 1], x[i]);
         }
+        l += sum[0] + sum[1];
         fence();
         __builtin_amdgcn_s_setprio(0);
-        float a[RT][2];
+        float a[2];
 #pragma unroll
         for (int c = 0; c < 2 * kD; ++c) {
-#pragma unroll
-          for (int n = 0; n < RT; ++n) o[n][c % kD] = mfma32<T>(vf[c], pr[n][c / kD], o[n][c % kD]);
+          o[c % kD] = mfma32<T>(vf[c], pr[c / kD], o[c % kD]);
           fence();
           if (c >= kD) {  // the scores are there: their maxima
 #pragma unroll
-            for (int n = 0; n < RT; ++n)
-#pragma unroll
-              for (int i = 16 * (c - kD) / kD; i < 16 * (c - kD + 1) / kD; ++i)
-                a[n][i & 1] = i < 2 ? st[1 - B][n][i] : fmaxf(a[n][i & 1], st[1 - B][n][i]);
+            for (int i = 16 * (c - kD) / kD; i < 16 * (c - kD + 1) / kD; ++i)
+              a[i & 1] = i < 2 ? st[1 - B][i] : fmaxf(a[i & 1], st[1 - B][i]);
             fence();
           }
         }
-#pragma unroll
-        for (int n = 0; n < RT; ++n) {
-          const float top = fmaxf(a[n][0], a[n][1]);
-          most[n] = fmaxf(top, lane_xor<32>(top)) * A.scale;
-        }
-        rescale(most);
+        const float top = fmaxf(a[0], a[1]);
+        rescale(fmaxf(top, lane_xor<32>(top)) * A.scale);
       };
       // no way round a step's products in here: the outputs stay where they are
       for (; j + 2 < clear; j += 2) {
@@ -928,8 +911,7 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
       if (j + 1 < clear) {
         body(std::integral_constant<int, 0>(), j);
         ++j;
-#pragma unroll
-        for (int n = 0; n < RT; ++n) st[0][n] = st[1][n];
+        st[0] = st[1];
       }
       advance(j);
       probabilities(st[0]);
@@ -942,15 +924,11 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
       const int key = from + 32 * j;
       const uint32_t there = paged(key);
       scores(j, st[0]);
+      const uint32_t v = seen(key, there) >> (4 * h);
 #pragma unroll
-      for (int n = 0; n < RT; ++n) {
-        const uint32_t v = seen(n, key, there) >> (4 * h);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!(v >> (8 * (i >> 2) + (i & 3)) & 1)) st[0][n][i] = -INFINITY;
-      }
-      maxima(st[0], most);
-      rescale(most);
+      for (int i = 0; i < 16; ++i)
+        if (!(v >> (8 * (i >> 2) + (i & 3)) & 1)) st[0][i] = -INFINITY;
+      rescale(maximum(st[0]));
       probabilities(st[0]);
       products(j);
       advance(j);
@@ -972,41 +950,36 @@ __global__ __launch_bounds__(64 * W) void lb_attn_tile_kernel(const LbAttnArgs A
         for (int r = 0; r < 32; ++r) {
           const int page = page_at(at + r);
           const char* const src = v_head + (is_page(page) ? page : 0) * P.page + ((at + r) & mask) * P.slot;
+          const bool mine = seen(at, there) >> r & 1;
 #pragma unroll
-          for (int n = 0; n < RT; ++n) {
-            const bool mine = seen(n, at, there) >> r & 1;
+          for (int d = 0; d < kD; ++d)
 #pragma unroll
-            for (int d = 0; d < kD; ++d)
+            for (int i = 0; i < 4; ++i) {
+              const f32x4 f = odd_values<T>(src, 32 * d + 8 * i + 4 * h, A.dim, mine);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const f32x4 f = odd_values<T>(src, 32 * d + 8 * i + 4 * h, A.dim, mine);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][d][4 * i + e] += f[e];
-              }
-          }
+              for (int e = 0; e < 4; ++e) o[d][4 * i + e] += f[e];
+            }
         }
       }
     }
   }
+  l += lane_xor<32>(l);
+  if (in) {
 #pragma unroll
-  for (int n = 0; n < RT; ++n) {
-    l[n] += lane_xor<32>(l[n]);
-    const int row = first_row + 32 * n + r32;
-    if (row < all_rows) {
+    for (int d = 0; d < kD; ++d)
 #pragma unroll
-      for (int d = 0; d < kD; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f32x4 v = {o[n][d][4 * i], o[n][d][4 * i + 1], o[n][d][4 * i + 2], o[n][d][4 * i + 3]};
-          store_part<T>(A, p, kv_head, kRows, part, parts, row, row - block * kRows, 32 * d + 8 * i + 4 * h, v, m[n], l[n]);
-        }
-    }
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 v = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+        store_part<T>(A, p, kv_head, kRows, part, parts, row, row - block * kRows, 32 * d + 8 * i + 4 * h, v, m, l);
+      }
   }
 }
 
 // ------------------------------------------------------------------------- the join
 // Rows of the call whose keys were taken in parts.  A wave looks at `per` rows' records at once and joins those
-// with several parts, one after the other: eight times 64 / LD parts at once, four channels a lane.  A part in which a row saw nothing has no maximum, and a sum of 0 (or NaN).
+// with several parts, one after the other: eight times 64 / LD parts at once, four channels a lane.  A part in which a
+// row saw nothing has no maximum, and a sum of 0 (or NaN).  Latency bounds it, 4 us; of 15600 rows in
+// some four parts of 128 channels 16 us, 3.4 TB/s.
 template <typename T, int LD>
 __global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, int rows, int per) {
   constexpr int kSets = 64 / LD;
@@ -1098,16 +1071,18 @@ void launch_stream(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stre
   launch_join<T, DP / 4>(a, plan, stream);
 }
 
-template <typename T, int DP, int RT, int KT, int W>
+template <typename T, int DP, int KT, int W>
 void launch_tile(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
-  hipLaunchKernelGGL((lb_attn_tile_kernel<T, DP, RT, KT, W>), dim3((unsigned)plan.grid), dim3(64 * W), 0, stream, a);
+  hipLaunchKernelGGL((lb_attn_tile_kernel<T, DP, KT, W>), dim3((unsigned)plan.grid), dim3(64 * W), 0, stream, a);
   launch_join<T, DP / 4>(a, plan, stream);
 }
 
 template <typename T, int DP, int W>
 void launch_rows(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
-  if (plan.rows > 32)
-    launch_tile<T, DP, 1, DP == 256 ? 1 : 2, DP == 256 ? 4 : 8>(a, plan, stream);
+  if (plan.rows == 256) {
+    if constexpr (DP == 128) launch_tile<T, DP, 2, 8>(a, plan, stream);
+  } else if (plan.rows == 128)
+    launch_tile<T, DP, DP == 256 ? 1 : 2, 4>(a, plan, stream);
   else if (plan.rows == 16)
     launch_stream<T, DP, 1, W>(a, plan, stream);
   else
@@ -1129,20 +1104,24 @@ void launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream
 // Rows of a workgroup by the rows that a sequence has on average.  bf16, some 2000 keys: 36 rows (64 / 8 heads of 128,
 // 16 sequences) in blocks of 16, 32 and 256 take 33, 34 and 45 us, 75 rows 45 and 45 in 32 and 256, 100 rows 59 and 46;
 // 24 rows of 40 heads in 16 and 32 take 29 and 26; 75 rows of 8 heads of 256, 54 and 94 us in 32 and 128, of 16 heads of 64,
-// 31 and 41 in 32 and 256.  (64 rows a workgroup of few rows leave no registers: 51 us for the first.)  A sequence of n rows has at most
-// n group / rows + 1 blocks, and `target` / kv_heads parts at most are added over all of them; sequences
-// with several parts have at most twice their share of them.
+// 31 and 41 in 32 and 256.  (64 rows a workgroup of few rows leave no registers: 51 us for the first.)
+// Of many rows, blocks of 128, two at a time on a compute unit, read the keys twice as often as those of 256, and keep
+// fewer waves waiting where keys end soon: heads of 128, 3 prompts of 1500 81 and 91 us, one of 512 21 and 26, 4000 tokens on
+// 4100 keys 848 and 814, 100 on 8000 126 and 111; heads of 64, 4000 tokens 77 and 85, 16000 2500 and 2610.
+// A sequence of n rows has at most n group / rows + 1 blocks, and `target` / kv_heads parts at most are added over all
+// of them; sequences with several parts have at most twice their share of them.
 LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int64_t capacity, int heads, int kv_heads, int dim) {
   LbAttnPlan p;
   const int64_t group = heads / kv_heads, mean = (tokens * group + seqs - 1) / seqs;
-  p.rows = mean <= 16 ? 16 : mean <= (dim > 64 && dim <= 128 ? 80 : 112) ? 32 : dim <= 128 ? 256 : 128;
+  p.rows = mean <= 16 ? 16 : mean <= (dim > 64 && dim <= 128 ? 80 : 112) ? 32 : 128;
+  if (p.rows == 128 && dim > 64 && dim <= 128 && (mean > 4096 || capacity > 4096)) p.rows = 256;
   // workgroups at once: by their LDS and registers
-  p.round = p.rows > 32 ? 256 : dim <= 64 && p.rows == 16 ? 1024 : 512;
+  p.round = p.rows == 256 || (p.rows == 128 && dim > 128) ? 256 : dim <= 64 && p.rows == 16 ? 1024 : 512;
   p.least = p.rows > 32 ? 1024 : 256;
   // blocks of all sequences, at most, and what is shared out for so many; an empty workgroup costs a nanosecond (6000 of
   // them for one token 5 us)
   const int64_t blocks = std::min(tokens * group / p.rows + seqs, tokens * group);
-  const int64_t most = p.rows > 32 ? 512 : p.rows == 16 ? 1536 : 1024;
+  const int64_t most = p.rows > 32 ? 2 * p.round : p.rows == 16 ? 1536 : 1024;
   p.target = p.rows > 32 ? (int)most : (int)std::min<int64_t>(most, p.round * (1 + 4 * blocks * kv_heads / p.round));
   const int64_t parts = (capacity + p.least - 1) / p.least;
   p.join = parts > 1;

@@ -306,6 +306,7 @@ ATTEND = [
     ([(9, 4000), (1, 1)], 4, 1, 256, 64), ([(3, 2500)], 2, 2, 64, 8), ([(300, 40)], 3, 1, 64, 16), ([(1, 3000)], 40, 1, 24, 16),
     ([(130, 1111), (257, 0)], 4, 2, 128, 16), ([(1, 700), (2, 90)], 64, 1, 128, 1024), ([(100, 6000)], 4, 1, 128, 64),
     ([(40, 2500), (41, 2400)], 16, 4, 64, 32), ([(200, 1500)], 1, 1, 256, 128), ([(90, 40), (300, 7), (513, 0), (1, 9)], 2, 2, 96, 8),
+    ([(300, 4200), (300, 10), (0, 3)], 4, 2, 112, 32), ([(600, 100)], 8, 1, 128, 64), ([(140, 4500), (31, 225)], 4, 1, 128, 16),
 ]
 
 
@@ -328,7 +329,8 @@ def tree_words(rng, rows):
 
 
 TREES = [([(1, 0)], 1, 1, 64, 8), ([(2, 0), (16, 31)], 4, 4, 128, 16), ([(64, 0)], 2, 1, 128, 8), ([(64, 1000), (13, 64), (0, 4), (27, 1)], 8, 2, 128, 64),
-         ([(33, 4099)], 4, 1, 64, 32), ([(61, 77), (5, 3)], 3, 1, 256, 16), ([(16, 2000)], 2, 2, 80, 64), ([(64, 31), (64, 32), (64, 33)], 8, 8, 96, 8), ([(64, 5000)], 4, 1, 128, 64), ([(50, 3000), (64, 9)], 8, 2, 256, 16)]
+         ([(33, 4099)], 4, 1, 64, 32), ([(61, 77), (5, 3)], 3, 1, 256, 16), ([(16, 2000)], 2, 2, 80, 64), ([(64, 31), (64, 32), (64, 33)], 8, 8, 96, 8), ([(64, 5000)], 4, 1, 128, 64), ([(50, 3000), (64, 9)], 8, 2, 256, 16),
+         ([(64, 4300), (5, 70), (33, 0)], 8, 1, 72, 16)]
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
@@ -431,7 +433,7 @@ def test_what_is_not_seen_has_no_part(attn, rows, value, dt):
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
-@pytest.mark.parametrize("rows,cached,heads,dim", [(6, 40, 2, 128), (300, 40, 1, 128), (200, 2000, 2, 64), (150, 1030, 1, 256), (40, 900, 2, 256)])
+@pytest.mark.parametrize("rows,cached,heads,dim", [(6, 40, 2, 128), (300, 40, 1, 128), (300, 4200, 2, 128), (200, 2000, 2, 64), (150, 1030, 1, 256), (40, 900, 2, 256)])
 def test_values_that_are_seen_keep_their_infinities(attn, rows, cached, heads, dim, dt):
     """Infinite values of one sign in a channel give that infinity to the rows that see them, of both signs NaN; among
     the keys before the rows they reach every row."""
@@ -452,16 +454,17 @@ def test_values_that_are_seen_keep_their_infinities(attn, rows, cached, heads, d
 
 def test_entries_that_name_no_page(attn):
     """Their keys are not attended and not written, and nothing else is touched."""
-    for rows in (1, 100):
-        case("bad entries", rows)
-        p = Paged(attn, 10, [(rows, 300), (1, 50)], 2, 64, 16, torch.bfloat16)
+    for rows, cached in ((1, 300), (100, 300), (100, 4300)):
+        dim = 128 if cached > 4096 else 64
+        case("bad entries", rows, cached)
+        p = Paged(attn, 10, [(rows, cached), (1, 50)], 2, dim, 16, torch.bfloat16)
         pages = p.cache.k.shape[0]
         p.table[0, 2], p.table[0, 5], p.table[0, -2], p.table[1, 1] = -1, pages, 2 ** 31 - 1, -2 ** 31
         p.say()
-        q = randn(11, p.tokens, 4, 64).bfloat16()
+        q = randn(11, p.tokens, 4, dim).bfloat16()
         out, lse = run_attention(attn, p, q)
-        check_attention(out, lse, q, p, 0.125)
-        k, v = randn(12, p.tokens, 2, 64).bfloat16(), randn(13, p.tokens, 2, 64).bfloat16()
+        check_attention(out, lse, q, p, dim ** -0.5)
+        k, v = randn(12, p.tokens, 2, dim).bfloat16(), randn(13, p.tokens, 2, dim).bfloat16()
         want = oa.append(f64(p.cache.k), f64(p.cache.v), f64(k), f64(v), p.starts, p.lens, p.table)
         attn.littlebit_cache_append(p.cache, p.batch, k.cuda(), v.cuda())
         assert np.array_equal(f64(p.cache.k), want[0]) and np.array_equal(f64(p.cache.v), want[1])
