@@ -119,6 +119,34 @@ __device__ __forceinline__ int scan64(int v, int* total) {
 __device__ __forceinline__ int blocks_of(const Span& s, int group, int rows) { return (s.rows * group + rows - 1) / rows; }
 __device__ __forceinline__ int parts_of(int keys, int span) { return max(1, (keys + span - 1) / span); }
 
+__device__ __forceinline__ Span read_span(const LbAttnArgs& A, int seq) {
+  Span s = span_of(A.pages, min(seq, A.pages.seqs - 1), (int)A.tokens);
+  if (seq >= A.pages.seqs) s.rows = 0;
+  return s;
+}
+// Keys that a sequence's blocks take, on the mean: causal rows see half of the rows' own.
+template <bool MANY>
+__device__ __forceinline__ float keys_of(const LbAttnArgs& A, const Span& s) {
+  return MANY && !A.tree ? (float)s.keys - 0.5f * (float)s.rows : (float)s.keys;
+}
+// Keys of a part of a sequence, at most `span`: all its parts as long as each other.
+template <int STEP>
+__device__ __forceinline__ int part_keys(const Span& s, int span) {
+  const int parts = parts_of(s.keys, span), even = (s.keys + parts - 1) / parts;
+  return max((even + STEP - 1) / STEP * STEP, STEP);
+}
+// Keys of a part, from the sums over all sequences of the blocks, and of the blocks' keys.
+template <bool MANY>
+__device__ __forceinline__ int span_from(const LbAttnArgs& A, float blocks, float units, bool* whole) {
+  const float round = (float)A.round;
+  blocks *= (float)A.kv_heads;
+  *whole = MANY && __builtin_amdgcn_readfirstlane(blocks > 0.5f * round);
+  const float rounds = MANY ? 2.0f : 1.0f + floorf(4.0f * blocks / round);
+  const float share = fminf(fmaxf(round * rounds - blocks, 0.5f * round), (float)A.target);
+  units *= (float)A.kv_heads / share;
+  return __builtin_amdgcn_readfirstlane(*whole ? 1 << 30 : max(A.least, units < 1e9f ? (int)units + 1 : 1 << 30));
+}
+
 // The place of item `item`.  A part has the keys, in steps of STEP, that spread all sequences' keys (times their
 // blocks of rows) over the workgroups that run at once, `round` of them, and no fewer than `least`; the parts of a
 // sequence are as long as each other.  Parts are rounded up, at most one for each block, so that `round` less the
@@ -126,40 +154,44 @@ __device__ __forceinline__ int parts_of(int keys, int span) { return max(1, (key
 // that the last parts are short beside the whole; of many rows (MANY), whose parts cost more to join, not at all,
 // and the blocks that see the most come first.  Where blocks of many rows are few, lengths of parts are compared by the
 // rounds they take (2 sequences of 64 rows over 16000 keys of 64 / 8 heads of 128: 92 -> 71 us, 500 tokens on 4000 of 16 / 4
-// heads of 256 104 -> 73; 3 of 200 over 20000 of 32 / 8 heads, though, 213 -> 221).  Up to 64 sequences are read once.
+// heads of 256 104 -> 73; 3 of 200 over 20000 of 32 / 8 heads, though, 213 -> 221).  Every workgroup finds its place by
+// itself, up to 64 sequences at once; of more than kFewSeqs, a kernel before this one has added them up (`groups`).
 template <int STEP, bool MANY>
 __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int item) {
   const int lane = threadIdx.x & 63;
   const int seqs = A.pages.seqs;
-  auto read = [&](int from) __attribute__((always_inline)) {
-    Span s = span_of(A.pages, min(from + lane, seqs - 1), (int)A.tokens);
-    if (from + lane >= seqs) s.rows = 0;
-    return s;
-  };
-  // keys that a sequence's blocks take, on the mean: causal rows see half of the rows' own
-  auto keys_of = [&](const Span& s) __attribute__((always_inline)) {
-    return MANY && !A.tree ? (float)s.keys - 0.5f * (float)s.rows : (float)s.keys;
-  };
-  const Span first = read(0);
-  // in floating point, in one order everywhere: all workgroups get the same
-  float blocks_all = (float)blocks_of(first, A.group, rows);
-  float units = keys_of(first) * blocks_all;
-  for (int from = 64; from < seqs; from += 64) {
-    const Span s = read(from);
-    const float blocks = (float)blocks_of(s, A.group, rows);
-    blocks_all += blocks;
-    units += keys_of(s) * blocks;
+  int begin = 0, end = seqs, items = 0, slots = 0, span;
+  bool whole = false;
+  if (A.groups) {
+    // the last 64 sequences that begin at or before the item
+    int first = 0, count = (seqs + 63) >> 6;
+    while (count > 1) {
+      const int step = (count + 63) >> 6, at = lane * step;
+      const uint64_t b = __ballot(at < count && A.groups[2 + 2 * (first + min(at, count - 1))] <= item);
+      const int last = b ? 63 - __builtin_clzll(b) : 0;
+      first += last * step;
+      count = min(step, count - last * step);
+    }
+    span = A.groups[0];
+    items = A.groups[2 + 2 * first];
+    slots = A.groups[3 + 2 * first];
+    begin = 64 * first;
+    end = min(begin + 64, seqs);
   }
-  blocks_all = wave_sum(blocks_all) * (float)A.kv_heads;
-  const float round = (float)A.round;
-  const bool whole = MANY && __builtin_amdgcn_readfirstlane(blocks_all > 0.5f * round);
-  const float rounds = MANY ? 2.0f : 1.0f + floorf(4.0f * blocks_all / round);
-  const float share = fminf(fmaxf(round * rounds - blocks_all, 0.5f * round), (float)A.target);
-  units = wave_sum(units) * (float)A.kv_heads / share;
-  const int want = whole ? 1 << 30 : max(A.least, units < 1e9f ? (int)units + 1 : 1 << 30);
-  Place p;
-  p.seq = -1;
-  int span = __builtin_amdgcn_readfirstlane(want);
+  const Span first = read_span(A, begin + lane);
+  if (!A.groups) {
+    // in floating point, in one order everywhere: all workgroups get the same
+    float blocks = (float)blocks_of(first, A.group, rows);
+    float units = keys_of<MANY>(A, first) * blocks;
+    for (int from = 64; from < seqs; from += 64) {
+      const Span s = read_span(A, from + lane);
+      const float b = (float)blocks_of(s, A.group, rows);
+      blocks += b;
+      units += keys_of<MANY>(A, s) * b;
+    }
+    blocks = wave_sum(blocks);
+    span = span_from<MANY>(A, blocks, wave_sum(units), &whole);
+  }
   if (MANY && !whole && seqs <= 64) {
     // a lane each: the longest sequence in lane + 1 parts, and the others in parts of that length
     const int longest = __builtin_amdgcn_readfirstlane((int)wave_max(first.rows > 0 ? (float)first.keys : 0.0f));
@@ -173,17 +205,17 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
       joined += parts > 1 ? b * parts : 0;
     }
     const bool fits = all <= (int)(gridDim.x / A.kv_heads) && joined <= A.slots;
-    const float rounds = ceilf((float)all * (float)A.kv_heads / round);
+    const float rounds = ceilf((float)all * (float)A.kv_heads / (float)A.round);
     const float cost = lane == 0 || fits ? rounds * (float)(even + kPartKeys) : INFINITY;
     const uint64_t best = __ballot(cost == -wave_max(-cost));
     span = __builtin_amdgcn_readlane(mine, __builtin_ctzll(best | 1ull << 63));
   }
-  int items = 0, slots = 0;
-  for (int from = 0; from < seqs; from += 64) {
-    const Span s = from ? read(from) : first;
+  Place p;
+  p.seq = -1;
+  for (int from = begin; from < end; from += 64) {
+    const Span s = from > begin ? read_span(A, from + lane) : first;
     const int blocks = blocks_of(s, A.group, rows);
-    const int even = (s.keys + parts_of(s.keys, span) - 1) / parts_of(s.keys, span);
-    const int own = max((even + STEP - 1) / STEP * STEP, STEP);
+    const int own = part_keys<STEP>(s, span);
     const int parts = parts_of(s.keys, own);
     int all, all_slots;
     int before = items + scan64(blocks * parts, &all);
@@ -221,6 +253,58 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
     slots += all_slots;
   }
   return p;
+}
+
+// Of many sequences, what every workgroup would add up, once: [0] the keys of a part, [2 + 2 g] and [3 + 2 g] the items and
+// the slots before the 64 sequences from 64 g on.  One workgroup; latency bounds it.  One token
+// of each sequence, 64 / 8 heads of 128, bf16, without and with it: 256 over 1000 keys 215 and 211 us, 1024 906 and 782, 4096
+// over 500 4780 and 1590 (5.3 TB/s).
+constexpr int kFewSeqs = 128;
+template <int STEP, bool MANY>
+__global__ __launch_bounds__(1024) void lb_attn_groups_kernel(const LbAttnArgs A, int* __restrict__ out, int rows) {
+  __shared__ float2 sums[16];
+  __shared__ int2 totals[1024], waves[16];
+  const int w = wave_id(), lane = threadIdx.x & 63, t = threadIdx.x;
+  const int groups = (A.pages.seqs + 63) >> 6;
+  float blocks = 0.0f, units = 0.0f;
+  for (int g = w; g < groups; g += 16) {
+    const Span s = read_span(A, 64 * g + lane);
+    const float b = (float)blocks_of(s, A.group, rows);
+    blocks += b;
+    units += keys_of<MANY>(A, s) * b;
+  }
+  blocks = wave_sum(blocks);
+  units = wave_sum(units);
+  if (lane == 0) sums[w] = float2{blocks, units};
+  __syncthreads();
+  blocks = units = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    blocks += sums[i].x;
+    units += sums[i].y;
+  }
+  bool whole;
+  const int span = span_from<MANY>(A, blocks, units, &whole);
+  for (int g = w; g < groups; g += 16) {
+    const Span s = read_span(A, 64 * g + lane);
+    const int b = blocks_of(s, A.group, rows), parts = parts_of(s.keys, part_keys<STEP>(s, span));
+    int2 all;
+    scan64(b * parts, &all.x);
+    scan64(parts > 1 ? b * parts : 0, &all.y);
+    if (lane == 0) totals[g] = all;
+  }
+  __syncthreads();
+  int2 all, before = t < groups ? totals[t] : int2{0, 0};
+  before.x = scan64(before.x, &all.x);
+  before.y = scan64(before.y, &all.y);
+  if (lane == 0) waves[w] = all;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) {
+    before.x += waves[i].x;
+    before.y += waves[i].y;
+  }
+  if (t < groups) *(int2*)(out + 2 + 2 * t) = before;
+  if (t == 0) out[0] = span;
 }
 
 // Keys that the rows of a block see, all of them together and each of them: those below `most`,
@@ -384,7 +468,8 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
   const int first_row = block * kRows, all_rows = p.s.rows * A.group;
   const Sight sight = sight_of(A, p.s, first_row, kRows);
   const int parts = parts_of(sight.most, p.span);
-  if (part >= parts || (parts > 1 && p.slot >= A.slots)) return;  // the latter: starts that name rows twice
+  // the latter: starts that name rows twice, whose sums may wrap as well
+  if (part >= parts || (parts > 1 && (uint32_t)p.slot >= (uint64_t)A.slots)) return;
   const int from = part * p.span, to = min(from + p.span, sight.most);
 
   const LbPages& P = A.pages;
@@ -658,7 +743,8 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void lb_attn_tile_kernel
   const int all_rows = p.s.rows * A.group;
   const Sight sight = sight_of(A, p.s, block * kRows, kRows);
   const int parts = parts_of(sight.most, p.span);
-  if (part >= parts || (parts > 1 && p.slot >= A.slots)) return;  // the latter: starts that name rows twice
+  // the latter: starts that name rows twice, whose sums may wrap as well
+  if (part >= parts || (parts > 1 && (uint32_t)p.slot >= (uint64_t)A.slots)) return;
   const int from = part * p.span, to = min(from + p.span, sight.most);
   const int first_row = block * kRows + 32 * w;
   // this wave's own rows: their keys end earlier, and may be seen by all of them later
@@ -1065,14 +1151,21 @@ void launch_join(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream
                      plan.rows, per);
 }
 
+template <int STEP, bool MANY>
+void launch_groups(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
+  if (a.groups) hipLaunchKernelGGL((lb_attn_groups_kernel<STEP, MANY>), dim3(1), dim3(1024), 0, stream, a, a.groups, plan.rows);
+}
+
 template <typename T, int DP, int NT, int W>
 void launch_stream(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
+  launch_groups<32 * W, false>(a, plan, stream);
   hipLaunchKernelGGL((lb_attn_stream_kernel<T, DP, NT, W>), dim3((unsigned)plan.grid), dim3(64 * W), 0, stream, a);
   launch_join<T, DP / 4>(a, plan, stream);
 }
 
 template <typename T, int DP, int KT, int W>
 void launch_tile(const LbAttnArgs& a, const LbAttnPlan& plan, hipStream_t stream) {
+  launch_groups<32 * KT, true>(a, plan, stream);
   hipLaunchKernelGGL((lb_attn_tile_kernel<T, DP, KT, W>), dim3((unsigned)plan.grid), dim3(64 * W), 0, stream, a);
   launch_join<T, DP / 4>(a, plan, stream);
 }
@@ -1127,13 +1220,18 @@ LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int64_t capacity, int heads, i
   p.join = parts > 1;
   const int64_t share = (p.target + kv_heads - 1) / kv_heads + 1;
   p.slots = p.join ? std::min(2 * share + 2, blocks * parts) : 0;
+  p.groups = seqs > kFewSeqs ? (seqs + 63) / 64 : 0;
   p.grid = std::min(share + blocks + 2, blocks * parts) * kv_heads;
   return p;
 }
 
-size_t lb_attn_workspace(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim) {
+size_t lb_attn_groups_at(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim) {
   if (!plan.join) return 0;
   return (size_t)plan.slots * kv_heads * plan.rows * (dim + 2) * sizeof(float) + (size_t)tokens * heads * 2 * sizeof(int);
+}
+
+size_t lb_attn_workspace(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim) {
+  return lb_attn_groups_at(plan, tokens, heads, kv_heads, dim) + (plan.groups ? (plan.groups + 1) * 2 * sizeof(int) : 0);
 }
 
 hipError_t lb_launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, int dtype, hipStream_t stream) {

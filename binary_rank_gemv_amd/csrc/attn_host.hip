@@ -315,7 +315,8 @@ lb_status littlebit_cache_append(const lb_cache* cache, const lb_cache_batch* ba
 size_t littlebit_cache_attention_workspace_bytes(const lb_cache* cache, const lb_cache_batch* batch, int64_t tokens,
                                                  int32_t heads) {
   if (!cache || !batch || tokens < 1 || tokens > kMaxTokens || cache->heads < 1 || cache->heads > kMaxHeads || heads < 1 ||
-      heads > kMaxHeads || heads % cache->heads || batch->seqs < 1 || batch->columns < 1 || cache->page_size < 1 || cache->dim < 2 || cache->dim > LB_HEAD_MAX_DIM)
+      heads > kMaxHeads || heads % cache->heads || batch->seqs < 1 || batch->seqs >= (1 << 16) || batch->columns < 1 ||
+      cache->page_size < 1 || cache->dim < 2 || cache->dim > LB_HEAD_MAX_DIM)
     return 0;
   return lb_attn_workspace(lb_attn_plan(tokens, batch->seqs, (int64_t)batch->columns * cache->page_size, heads, cache->heads, cache->dim), tokens, heads, cache->heads,
                            cache->dim);
@@ -350,6 +351,7 @@ lb_status littlebit_cache_attention_fwd(const lb_cache* cache, const lb_cache_ba
   a.tree = tree;
   a.lse = lse;
   a.partial = (float*)ws;
+  if (plan.groups) a.groups = (int*)((char*)ws + lb_attn_groups_at(plan, tokens, q->heads, cache->heads, cache->dim));
   a.slots = plan.slots;
   a.tokens = tokens;
   a.heads = q->heads;

@@ -64,6 +64,7 @@ struct LbAttnArgs {
   const int64_t* tree;
   float* lse;
   float* partial;          // the workspace
+  int* groups;             // in it, of many sequences: what every 64 of them have before them; or null
   long slots;
   long tokens;
   int heads, kv_heads, group, dim;
@@ -80,6 +81,7 @@ struct LbAttnPlan {
   int least;               // keys of a part, at least
   bool join;               // whether a sequence can have several parts
   long slots;              // workgroups whose results may have to be joined
+  int groups;              // 64 sequences each, where a kernel adds them up first; or 0
   long grid;
 };
 
@@ -88,5 +90,6 @@ hipError_t lb_launch_rope(LbRopeArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_rope_bwd(const LbRopeBwdArgs& a, int dtype, hipStream_t stream);
 hipError_t lb_launch_accept(const LbPages& p, int heads, int dim, const int32_t* path, int columns, hipStream_t stream);
 LbAttnPlan lb_attn_plan(int64_t tokens, int seqs, int64_t capacity, int heads, int kv_heads, int dim);
+size_t lb_attn_groups_at(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim);
 size_t lb_attn_workspace(const LbAttnPlan& plan, int64_t tokens, int heads, int kv_heads, int dim);
 hipError_t lb_launch_attn(const LbAttnArgs& a, const LbAttnPlan& plan, int dtype, hipStream_t stream);

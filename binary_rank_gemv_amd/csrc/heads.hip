@@ -505,7 +505,8 @@ void launch_bwd(const LbRopeBwdArgs& a, hipStream_t stream) {
 // ------------------------------------------------------------------ accepted rows
 // A workgroup: the accepted rows of one head's keys or values, all in registers before the first is written: at
 // most PIECES 16-byte pieces a thread, eight for 64 rows of 256 channels.  Latency bounds it, and, of many
-// sequences, how many workgroups run at once: 48 trees, 40 heads of 128, 9 rows each, 9.7 us with room for 8 pieces, 4.4 with one.
+// sequences, how many workgroups run at once: 48 trees, 40 heads of 128, 9 rows each, 15 us with room for 8 pieces a thread,
+// 4.8 with one; one tree 2.9.
 template <int PIECES>
 __global__ __launch_bounds__(256) void lb_accept_kernel(const LbPages P, int dim, const int32_t* __restrict__ path,
                                                         int columns) {

@@ -98,7 +98,7 @@ typedef struct {
  * page_size], slot j % page_size.  All int32 on the device, read by the kernels:
  * one captured graph serves every content.
  *   table      seqs rows of `columns` entries, table_stride apart.  Entries past a
- *              sequence's keys are not read.
+ *              sequence's keys may hold anything.
  * Rows that belong to no sequence (before starts[0], from starts[seqs] on) are left
  * as they are in every output.  What the tables say wrongly cannot reach memory
  * outside the tensors: an entry that names no page, or a key past the last column,

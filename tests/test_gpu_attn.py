@@ -374,6 +374,19 @@ def test_many_sequences(attn):
         check_attention(out, lse, q, p, 0.125)
 
 
+@pytest.mark.parametrize("seqs,rows,heads,dim", [(129, 3, 2, 64), (2000, 3, 2, 128), (4200, 1, 1, 64), (200, 70, 4, 128), (150, 90, 2, 256)])
+def test_thousands_of_sequences(attn, seqs, rows, heads, dim):
+    """More than are added up by every workgroup, some long enough for several parts, some empty."""
+    case("thousands", seqs, rows)
+    rng = np.random.default_rng(seqs)
+    counts = [(int(rng.integers(0, rows + 1)), int(rng.integers(0, 40))) for _ in range(seqs)]
+    counts[0], counts[64], counts[65], counts[seqs - 1] = (rows, 1500), (0, 70), (rows, 0), (rows, 3000)
+    p = Paged(attn, seqs, counts, 1, dim, 16, torch.float16)
+    q = randn(seqs, p.tokens, heads, dim).half()
+    out, lse = run_attention(attn, p, q)
+    check_attention(out, lse, q, p, dim ** -0.5)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
 def test_scales(attn, scale):
     p = Paged(attn, 4, [(3, 100)], 1, 64, 16, torch.float16)
