@@ -6,14 +6,14 @@
 // The rows of a key head's group (tokens x heads that share it) are the columns of the
 // matrix steps, the keys their rows: S^T = K Q^T.  A lane then holds a few keys of one row, so
 // the row's maximum takes moves between few lanes, and what it holds after the exponential is its
-// operand of O^T = V^T P^T as it stands, with no move at all: which key a step's k-th place stands
-// for is free as long as both operands agree.  V^T is read from LDS through the transposing
-// read.
+// operand of O^T = V^T P^T as it stands: which key a step's k-th place stands for is free as long as
+// both operands agree.  V^T is read from LDS through the transposing read.
+// That operand is rounded to the values' type, since the matrix units take both in one: each
+// probability by half a step of it, relative; their sum is of the unrounded ones, in fp32 like all else.
 //
-// Work is spread by the keys that there are: every workgroup adds up all sequences' keys and takes as many as
-// leave its share to each of those that run at once, whatever the lengths; a sequence's parts
-// are joined by a second kernel.  All of that is computed on the device, so that a captured call
-// serves any lengths.
+// Work is spread by the keys that there are, whatever the lengths: from all sequences' keys follows how many a
+// workgroup takes, so that those that run at once have as many each; a sequence's parts are joined by a second
+// kernel.  All of that is computed on the device, so that a captured call serves any lengths.
 #include <algorithm>
 #include <type_traits>
 
