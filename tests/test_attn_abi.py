@@ -178,6 +178,7 @@ def test_workspace_sizes():
     assert A(C(), B(), 0, 4) == 0 and A(C(), B(), 3, 3) == 0 and A(None, B(), 3, 4) == 0 and A(C(), None, 3, 4) == 0
     assert A(C(heads=0), LONG, 3, 4) == 0 and A(C(), B(seqs=0), 3, 4) == 0 and A(C(), LONG, 3, 4) > 0
     assert A(C(), B(), 3, 4) == 0   # short sequences: nothing to join
+    assert A(C(), B(seqs=1 << 16), 3, 4) == 0 and 0 < A(C(), B(seqs=200), 300, 4) <= A(C(), B(seqs=60000), 300, 4)   # many: places to add up
 
 
 def test_binding_refuses_what_is_not_on_a_gpu():
