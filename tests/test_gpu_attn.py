@@ -672,6 +672,30 @@ def test_one_captured_step_serves_any_lengths(attn):
         assert torch.equal(p.cache.k, other.cache.k) and torch.equal(p.cache.v, other.cache.v)
 
 
+def test_a_captured_call_of_many_sequences(attn):
+    """More than every workgroup adds up by itself, captured once; one with several parts, others shorter by the replay."""
+    p = Paged(attn, 50, [(1, 20 + i % 60) for i in range(199)] + [(1, 2500)], 1, 64, 16, torch.float16)
+    q = randn(51, p.tokens, 2, 64).half()
+    q_gpu, out, lse = q.cuda(), torch.zeros(200, 2, 64, dtype=torch.float16, device="cuda"), torch.zeros(200, 2, device="cuda")
+    call = lambda: attn.littlebit_cache_attention_fwd(q_gpu, p.cache, p.batch, out=out, lse=lse)  # noqa: E731
+    with torch.cuda.stream(torch.cuda.Stream()):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    full = p.lens.copy()
+    for cut in (0, 1, 7, 1):
+        case("replay", cut)
+        p.lens[:] = np.maximum(full - cut * (np.arange(200) % 5) ** 2, 1)
+        p.say()
+        out.fill_(9.0)
+        lse.fill_(9.0)
+        graph.replay()
+        check_attention(out, lse, q, p, 0.125)
+        assert torch.equal(out, attn.littlebit_cache_attention_fwd(q_gpu, p.cache, p.batch))
+
+
 def test_rope_captured_with_its_backward(attn):
     x, dy, w = (randn(i, 50, 4, 64).half().cuda() for i in (1, 2, 3))
     w = (1 + w[0, 0] / 4).contiguous()
