@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "attn_common.h"
+#include "attn_split.h"
 
 using namespace lbh;
 
@@ -116,35 +117,16 @@ __device__ __forceinline__ int scan64(int v, int* total) {
   return s - v;
 }
 
-__device__ __forceinline__ int blocks_of(const Span& s, int group, int rows) { return (s.rows * group + rows - 1) / rows; }
-__device__ __forceinline__ int parts_of(int keys, int span) { return max(1, (keys + span - 1) / span); }
-
 __device__ __forceinline__ Span read_span(const LbAttnArgs& A, int seq) {
   Span s = span_of(A.pages, min(seq, A.pages.seqs - 1), (int)A.tokens);
   if (seq >= A.pages.seqs) s.rows = 0;
   return s;
 }
-// Keys that a sequence's blocks take, on the mean: causal rows see half of the rows' own.
-template <bool MANY>
-__device__ __forceinline__ float keys_of(const LbAttnArgs& A, const Span& s) {
-  return MANY && !A.tree ? (float)s.keys - 0.5f * (float)s.rows : (float)s.keys;
-}
-// Keys of a part of a sequence, at most `span`: all its parts as long as each other.
-template <int STEP>
-__device__ __forceinline__ int part_keys(const Span& s, int span) {
-  const int parts = parts_of(s.keys, span), even = (s.keys + parts - 1) / parts;
-  return max((even + STEP - 1) / STEP * STEP, STEP);
-}
 // Keys of a part, from the sums over all sequences of the blocks, and of the blocks' keys.
 template <bool MANY>
-__device__ __forceinline__ int span_from(const LbAttnArgs& A, float blocks, float units, bool* whole) {
-  const float round = (float)A.round;
-  blocks *= (float)A.kv_heads;
-  *whole = MANY && __builtin_amdgcn_readfirstlane(blocks > 0.5f * round);
-  const float rounds = MANY ? 2.0f : 1.0f + floorf(4.0f * blocks / round);
-  const float share = fminf(fmaxf(round * rounds - blocks, 0.5f * round), (float)A.target);
-  units *= (float)A.kv_heads / share;
-  return __builtin_amdgcn_readfirstlane(*whole ? 1 << 30 : max(A.least, units < 1e9f ? (int)units + 1 : 1 << 30));
+__device__ __forceinline__ int span_of_sums(const LbAttnArgs& A, float blocks, float units, bool* whole) {
+  *whole = __builtin_amdgcn_readfirstlane(is_whole<MANY>(blocks * (float)A.kv_heads, (float)A.round));
+  return __builtin_amdgcn_readfirstlane(span_from<MANY>(blocks, units, A.kv_heads, A.round, A.target, A.least));
 }
 
 // The place of item `item`.  A part has the keys, in steps of STEP, that spread all sequences' keys (times their
@@ -181,22 +163,22 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
   const Span first = read_span(A, begin + lane);
   if (!A.groups) {
     // in floating point, in one order everywhere: all workgroups get the same
-    float blocks = (float)blocks_of(first, A.group, rows);
-    float units = keys_of<MANY>(A, first) * blocks;
+    const int own_blocks = blocks_of(first.rows, A.group, rows);
+    float blocks = (float)own_blocks, units = units_of(first.keys, own_blocks);
     for (int from = 64; from < seqs; from += 64) {
       const Span s = read_span(A, from + lane);
-      const float b = (float)blocks_of(s, A.group, rows);
-      blocks += b;
-      units += keys_of<MANY>(A, s) * b;
+      const int b = blocks_of(s.rows, A.group, rows);
+      blocks += (float)b;
+      units += units_of(s.keys, b);
     }
     blocks = wave_sum(blocks);
-    span = span_from<MANY>(A, blocks, wave_sum(units), &whole);
+    span = span_of_sums<MANY>(A, blocks, wave_sum(units), &whole);
   }
   if (MANY && !whole && seqs <= 64) {
     // a lane each: the longest sequence in lane + 1 parts, and the others in parts of that length
     const int longest = __builtin_amdgcn_readfirstlane((int)wave_max(first.rows > 0 ? (float)first.keys : 0.0f));
     const int even = (longest / (lane + 1) + STEP) / STEP * STEP, mine = lane ? even : 1 << 30;
-    const int own_blocks = blocks_of(first, A.group, rows);
+    const int own_blocks = blocks_of(first.rows, A.group, rows);
     int all = 0, joined = 0;
     for (uint64_t left = __ballot(own_blocks > 0); left; left &= left - 1) {
       const int l = __builtin_ctzll(left);
@@ -214,8 +196,8 @@ __device__ __forceinline__ Place place_of(const LbAttnArgs& A, int rows, int ite
   p.seq = -1;
   for (int from = begin; from < end; from += 64) {
     const Span s = from > begin ? read_span(A, from + lane) : first;
-    const int blocks = blocks_of(s, A.group, rows);
-    const int own = part_keys<STEP>(s, span);
+    const int blocks = blocks_of(s.rows, A.group, rows);
+    const int own = part_keys<STEP>(s.keys, span);
     const int parts = parts_of(s.keys, own);
     int all, all_slots;
     int before = items + scan64(blocks * parts, &all);
@@ -273,9 +255,9 @@ __global__ __launch_bounds__(1024) void lb_attn_groups_kernel(const LbAttnArgs A
   float blocks = 0.0f, units = 0.0f;
   for (int g = w; g < groups; g += 16) {
     const Span s = read_span(A, 64 * g + lane);
-    const float b = (float)blocks_of(s, A.group, rows);
-    blocks += b;
-    units += keys_of<MANY>(A, s) * b;
+    const int b = blocks_of(s.rows, A.group, rows);
+    blocks += (float)b;
+    units += units_of(s.keys, b);
   }
   blocks = wave_sum(blocks);
   units = wave_sum(units);
@@ -288,10 +270,10 @@ __global__ __launch_bounds__(1024) void lb_attn_groups_kernel(const LbAttnArgs A
     units += sums[i].y;
   }
   bool whole;
-  const int span = span_from<MANY>(A, blocks, units, &whole);
+  const int span = span_of_sums<MANY>(A, blocks, units, &whole);
   for (int g = w; g < groups; g += 16) {
     const Span s = read_span(A, 64 * g + lane);
-    const int b = blocks_of(s, A.group, rows), parts = parts_of(s.keys, part_keys<STEP>(s, span));
+    const int b = blocks_of(s.rows, A.group, rows), parts = parts_of(s.keys, part_keys<STEP>(s.keys, span));
     int2 all;
     scan64(b * parts, &all.x);
     scan64(parts > 1 ? b * parts : 0, &all.y);

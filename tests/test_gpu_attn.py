@@ -789,3 +789,55 @@ def test_binding_refuses(attn):
         with pytest.raises((ValueError, RuntimeError)):
             print("[refusal]", i, flush=True)
             call()
+
+
+# ------------------------------------------------------------------------------------- long prompts among many others
+
+class Packed(Paged):
+    """The same with as many pages as the keys need; what the table names behind a sequence's keys is another's."""
+
+    def __init__(self, attn, seed, counts, kv, dim, page, t):
+        self.counts, self.page, self.t = counts, page, t
+        rng = np.random.default_rng(seed)
+        self.starts = np.concatenate([[0], np.cumsum([n for n, _ in counts])]).astype(int)
+        self.lens = np.array([n + c for n, c in counts])
+        self.tokens = int(self.starts[-1])
+        used = -(-self.lens // page)
+        pages = int(used.sum()) + 2
+        order = rng.permutation(pages)
+        self.table = rng.integers(0, pages, (len(counts), max(1, int(used.max()))))
+        at = 0
+        for i, n in enumerate(used):
+            self.table[i, :n] = order[at:at + n]
+            at += n
+        shape = (pages, kv, page, dim)
+        k, v = (torch.from_numpy(rng.standard_normal(shape, dtype=np.float32)).to(t).cuda() for _ in range(2))
+        self.cache = attn.LittleBitCache(k, v)
+        self.batch = attn.CacheBatch(ints(self.starts.tolist()), ints(self.lens.tolist()), ints(self.table.tolist()))
+
+
+def check_sampled(out, lse, q, p, scale, picked):
+    """check_attention of some rows: each, with the keys that it sees, as a sequence of its own."""
+    place = oa.rows(p.starts, p.tokens)
+    one = Packed.__new__(Packed)
+    one.t, one.cache, one.page = p.t, p.cache, p.page
+    one.starts = np.arange(len(picked) + 1)
+    one.lens = np.array([p.lens[place[r][0]] - p.counts[place[r][0]][0] + place[r][1] + 1 for r in picked])
+    one.table = p.table[[place[r][0] for r in picked]]
+    check_attention(out[picked], lse[picked], q[picked], one, scale)
+
+
+@pytest.mark.parametrize("counts,heads,kv,dim", [
+    ([(5600, 3400)] + [(1, 999)] * 69, 4, 1, 64), ([(20000, 0)] + [(1, 0)] * 69, 1, 1, 64), ([(20000, 0)] + [(10, 0)] * 64, 1, 1, 64),
+    ([(9000, 0)] + [(1, 69)] * 140, 2, 1, 64), ([(8192, 0)] + [(0, 0)] * 64, 4, 1, 128), ([(6000, 100)] + [(3, 37)] * 130, 4, 1, 256)])
+def test_every_row_of_a_long_prompt_among_many_sequences(attn, counts, heads, kv, dim):
+    for name, order in (("first", counts), ("last", counts[::-1])):
+        case("long", name, counts[0], len(counts), heads, kv, dim)
+        p = Packed(attn, dim, order, kv, dim, 64, torch.float16)
+        q = randn(dim + 1, p.tokens, heads, dim, scale=1.5).to(p.t)
+        out, lse = run_attention(attn, p, q)
+        assert (lse != 55).all() and not (out == 55).all(2).any()   # no row was left out
+        long = 0 if name == "first" else len(counts) - 1
+        begin, end = p.starts[long], p.starts[long + 1]
+        picked = sorted({0, 1, p.tokens - 1, begin, end - 1, *range(begin, end, 397), *range(0, p.tokens, p.tokens // 7)})
+        check_sampled(out, lse, q, p, dim ** -0.5, picked)
