@@ -328,9 +328,11 @@ __device__ __forceinline__ void store_result(const LbAttnArgs& A, int token, int
 }
 
 // Where the parts of a row's result lie: part j in row first + j * step of the workspace.
-// One for each row of the call, written by its first part.
+// One for each row of the call, written by its first part.  A key head's parts are fewer than 2^16 (see the plan's
+// target), and so are the sequences.
 struct Parts {
-  int first, count;
+  int first;
+  uint32_t count;  // of the parts, and the sequence in the upper half
 };
 struct Workspace {
   float* sums;    // [slots][kv_heads][rows][dim]
@@ -360,7 +362,7 @@ __device__ __forceinline__ void store_part(const LbAttnArgs& A, const Place& p, 
     if (parts > 1 && d < A.dim) *(f32x4*)(w.sums + (long)at * A.dim + d) = o;
     if (d == 0) {
       if (parts > 1) w.ml[at] = float2{m, l};
-      if (part == 0 && A.slots > 0) w.parts[(long)token * A.heads + head] = Parts{at, parts};
+      if (part == 0 && A.slots > 0) w.parts[(long)token * A.heads + head] = Parts{at, (uint32_t)p.seq << 16 | (uint32_t)parts};
     }
   }
 }
@@ -1060,21 +1062,25 @@ __global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, i
   const long row0 = (blockIdx.x * 4l + w) * per;
   if (row0 >= all_rows) return;
   const Workspace ws = workspace_of(A, rows);
-  const int first_token = A.pages.starts[0], end_token = A.pages.starts[A.pages.seqs];
   const long mine = row0 + lane;
   Parts r = {0, 0};
   if (lane < per && mine < all_rows) r = ws.parts[mine];
   const long limit = A.slots * A.kv_heads * rows;
-  const int step = A.kv_heads * rows;
-  const long token = mine / A.heads;
-  // rows of no sequence have no record
-  bool several = lane < per && mine < all_rows && token >= first_token && token < end_token && r.count > 1;
-  several = several && r.first >= 0 && r.first + (r.count - 1l) * step < limit;
+  const int step = A.kv_heads * rows, count_of = r.count & 0xFFFF, seq = r.count >> 16 & 0xFFFF;
+  bool several = lane < per && mine < all_rows && count_of > 1 && seq < A.pages.seqs;
+  several = several && r.first >= 0 && r.first + (count_of - 1l) * step < limit;
+  if (several) {
+    // a row of no sequence has no record, and what lies in its place may be an earlier call's: a record stands if its
+    // sequence has the row in this call, which has written it then
+    const Span s = span_of(A.pages, seq, (int)A.tokens);
+    const int token = (int)(mine / A.heads);
+    several = token >= s.start && token < s.start + s.rows;
+  }
   const int set = lane / LD, d = 4 * (lane % LD);
   const bool in = d < A.dim;
   for (uint64_t left = __ballot(several); left; left &= left - 1) {
     const int l = __builtin_ctzll(left);
-    const int first = __builtin_amdgcn_readlane(r.first, l), count = __builtin_amdgcn_readlane(r.count, l);
+    const int first = __builtin_amdgcn_readlane(r.first, l), count = __builtin_amdgcn_readlane(count_of, l);
     float top = -INFINITY, total = 0.0f;
     f32x4 sum = {0, 0, 0, 0};
     // eight sets' loads at a time; behind the last part it again, with factor 0

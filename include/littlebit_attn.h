@@ -103,7 +103,9 @@ typedef struct {
  * as they are in every output.  What the tables say wrongly cannot reach memory
  * outside the tensors: an entry that names no page, or a key past the last column,
  * stands for no key (it is not attended, and nothing is written for it), and rows
- * outside of the call's tokens are not computed.
+ * outside of the call's tokens are not computed.  A sequence with a negative length or
+ * start, or with no row of the call, has none: what it would name is left as it is.
+ * starts must not fall; where they do, rows may be left out or taken twice.
  * 1 <= seqs < 2^16, columns <= 2^24, columns x page_size < 2^30.
  */
 typedef struct {

@@ -841,3 +841,47 @@ def test_every_row_of_a_long_prompt_among_many_sequences(attn, counts, heads, kv
         begin, end = p.starts[long], p.starts[long + 1]
         picked = sorted({0, 1, p.tokens - 1, begin, end - 1, *range(begin, end, 397), *range(0, p.tokens, p.tokens // 7)})
         check_sampled(out, lse, q, p, dim ** -0.5, picked)
+
+
+def attend_in(attn, p, q, out, lse, ws):
+    """The attention in a workspace of the caller's."""
+    ref = attn._ref
+    c, b = p.cache.c_struct(), p.batch.c_struct(0)
+    h = [attn._Heads(t.data_ptr(), *t.stride()[:2], t.shape[1]) for t in (q, out)]
+    attn._check(attn.LIB.littlebit_cache_attention_fwd(ref(c), ref(b), q.shape[0], ref(h[0]), None, q.shape[2] ** -0.5, ref(h[1]), lse.data_ptr(),
+                                                       ws.data_ptr(), ws.numel(), attn._raw_stream(0)))
+
+
+@pytest.mark.parametrize("rows,heads,dim", [(2, 4, 64), (60, 4, 128), (300, 2, 128)])
+@pytest.mark.parametrize("seqs", [3, 70, 140])
+def test_rows_of_no_sequence_are_not_joined_from_an_earlier_call(attn, rows, heads, dim, seqs):
+    """A workspace that holds another call's parts for every row; sequences with a negative length, a negative start, or
+    an end before their start have no rows then, and what they would name stays as it is."""
+    counts = [(rows, 3000), (rows, 2900), (rows, 3100)] + [(1, 5)] * (seqs - 3)
+    p = Packed(attn, 3, counts, 1, dim, 64, torch.bfloat16)
+    q = randn(4, p.tokens, heads, dim).bfloat16().cuda()
+    out, lse = torch.zeros_like(q), torch.zeros(p.tokens, heads, device="cuda")
+    c, b = p.cache.c_struct(), p.batch.c_struct(0)
+    ws = torch.zeros(attn.LIB.littlebit_cache_attention_workspace_bytes(attn._ref(c), attn._ref(b), p.tokens, heads), dtype=torch.uint8, device="cuda")
+    attend_in(attn, p, q, out, lse, ws)
+    full, full_lse = out.clone(), lse.clone()
+    starts, lens = p.batch.starts.clone(), p.batch.lens.clone()
+    for name, at, value, gone in (("length", 1, -1, range(rows, 2 * rows)), ("length", 0, -2 ** 31, range(rows)), ("start", 0, -3, range(rows)),
+                                  ("start", 0, 2 ** 31 - 1, range(rows)), ("start", 2, rows - 1, range(rows - 1, 2 * rows))):
+        case("no sequence", name, at, value)
+        p.batch.starts.copy_(starts)
+        p.batch.lens.copy_(lens)
+        (p.batch.lens if name == "length" else p.batch.starts)[at] = value
+        out.fill_(9.0)
+        lse.fill_(9.0)
+        attend_in(attn, p, q, out, lse, ws)
+        left = torch.zeros(p.tokens, dtype=torch.bool, device="cuda")
+        left[list(gone)] = True
+        if value == rows - 1:   # the first sequence ends a row earlier, the third begins where the second did not
+            assert (out[0:rows - 1] != 9).any(2).all() and torch.isfinite(out.float()).all()
+            continue
+        assert (out[left] == 9).all() and (lse[left] == 9).all()
+        others = ~left
+        # of other lengths of parts, perhaps: e of an output and of a probability on either side
+        assert (out[others].float() - full[others].float()).abs().max() <= 4 * half_step(p.t) * p.cache.v.float().abs().max()
+        assert (lse[others] - full_lse[others]).abs().max() <= 1e-3
