@@ -9,7 +9,8 @@
 // operand of O^T = V^T P^T as it stands: which key a step's k-th place stands for is free as long as
 // both operands agree.  V^T is read from LDS through the transposing read.
 // That operand is rounded to the values' type, since the matrix units take both in one: each
-// probability by half a step of it, relative; their sum is of the unrounded ones, in fp32 like all else.
+// probability by half a step of it, in fp16 by 2^-32 of the row's largest one at least; their sum is of the
+// unrounded ones, in fp32 like all else.
 //
 // Work is spread by the keys that there are, whatever the lengths: from all sequences' keys follows how many a
 // workgroup takes, so that those that run at once have as many each; a sequence's parts are joined by a second
@@ -32,7 +33,26 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kPartKeys = 512;  // what beginning, writing and joining a part of many rows costs, in keys
-constexpr float kSlack = 8.0f;  // log2: how far a maximum may grow before the sums are scaled down
+// The exponent that probabilities are relative to, in log2: kAhead below a row's largest score when it was last raised, and
+// it is raised when that has grown by more than kSlack since.  bf16 has fp32's range.  In fp16 a probability is at most
+// 2^15, half of what the type holds, and what is lost below its smallest step is 2^-32 of the row's largest one, of few rows
+// (whose matrix steps wait for memory) 2^-39.  (Of many rows, 12 ahead and 3 of slack: 2000 tokens on 2000 of 16 / 4 heads of
+// 256 165 -> 182 us, 4000 on 4100 of 64 / 8 heads of 128 814 -> 820.)
+template <typename T, bool MANY>
+constexpr float kAhead = __is_same(T, f16) ? MANY ? 7.0f : 14.0f : 0.0f;
+template <typename T, bool MANY>
+constexpr float kSlack = __is_same(T, f16) ? 15.0f - kAhead<T, MANY> : 8.0f;
+// Whether a row's largest score asks for it, and the one after that: not below the score by more than the two together
+// (of scores beyond 2^26, where neighbours are that far apart, it is the score itself).
+template <typename T, bool MANY>
+__device__ __forceinline__ bool grows(float most, float m) {
+  return most - m > kAhead<T, MANY> + kSlack<T, MANY>;
+}
+template <typename T, bool MANY>
+__device__ __forceinline__ float raised(float most, float m) {
+  const float up = most - kAhead<T, MANY>;
+  return fmaxf(m, grows<T, MANY>(most, up) ? most : up);
+}
 
 template <typename T>
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
@@ -599,8 +619,8 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
         for (int i = 1; i < 8; ++i) most = fmaxf(most, x[i]);
         most = fmaxf(most, lane_xor<16>(most));
         most = fmaxf(most, lane_xor<32>(most)) * A.scale;
-        if (__ballot(most > m[n] + kSlack)) {
-          const float up = fmaxf(m[n], most);
+        if (__ballot(grows<T, false>(most, m[n]))) {
+          const float up = raised<T, false>(most, m[n]);
           const float a = m[n] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[n] - up);
           m[n] = up;
           l[n] *= a;
@@ -869,8 +889,8 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void lb_attn_tile_kernel
     return fmaxf(a, lane_xor<32>(a)) * A.scale;
   };
   auto rescale = [&](float most) __attribute__((always_inline)) {
-    if (__ballot(most > m + kSlack)) {
-      const float up = fmaxf(m, most);
+    if (__ballot(grows<T, true>(most, m))) {
+      const float up = raised<T, true>(most, m);
       const float a = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - up);
       m = up;
       l *= a;

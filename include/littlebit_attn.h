@@ -171,8 +171,10 @@ lb_status littlebit_cache_append(const lb_cache *cache, const lb_cache_batch *ba
  *   ws         littlebit_cache_attention_workspace_bytes(...) bytes (may be 0, then ws may be
  *              NULL), 16-byte aligned.
  * Scores, softmax and sums are in fp32; the probabilities are rounded to the cache's type for
- * their product with the values (the matrix units take both in one type), relative to a maximum
- * that is at most 2^8 behind, so that they keep the type's digits.  The same call gives the same bits.
+ * their product with the values (the matrix units take both in one type), each by half a step of
+ * it.  In fp16, whose smallest step is a fixed one, those below 2^-21 of a row's largest are
+ * rounded by 2^-32 of that one at most.  scale q . k_j is 10^8 at most in size.  The same call
+ * gives the same bits.
  * tokens x q->heads <= 2^30, fewer where the grid holds no more.
  */
 size_t littlebit_cache_attention_workspace_bytes(const lb_cache *cache, const lb_cache_batch *batch,

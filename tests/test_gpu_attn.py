@@ -885,3 +885,59 @@ def test_rows_of_no_sequence_are_not_joined_from_an_earlier_call(attn, rows, hea
         # of other lengths of parts, perhaps: e of an output and of a probability on either side
         assert (out[others].float() - full[others].float()).abs().max() <= 4 * half_step(p.t) * p.cache.v.float().abs().max()
         assert (lse[others] - full_lse[others]).abs().max() <= 1e-3
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("keys,size", [(30000, 1), (900, 512)])   # in many parts, with maxima of their own, and in one
+@pytest.mark.parametrize("rows,heads,dim", [(1, 2, 64), (20, 1, 128), (3, 3, 256), (200, 1, 64), (150, 1, 256), (300, 1, 128)])
+def test_a_key_that_outweighs_all_others(attn, rows, heads, dim, keys, size, dt):
+    """The first key has nearly all of the softmax and a value of 0: the output is what the other keys add up to.  Half a step
+    of the type each, e, beside that of the output; of fp16 at least half its smallest step, 2^-25, of probabilities whose
+    largest is at least 2^14 (few rows) or 2^7 (many): 2^-39 or 2^-32 of it, for every key.  Sums of n terms: (n + 80) u."""
+    t = TYPES[dt]
+    for gap in (12.0, 20.0, 24.0, 25.2, 28.0):
+        case("outweighed", rows, heads, dim, keys, dt, gap)
+        p = Packed(attn, 60, [(rows, keys)], 1, dim, 64, t)
+        p.cache.k.zero_()
+        p.cache.v.abs_().mul_(size)
+        at = oa.place(0, 0, p.table, 64, p.cache.k.shape[0])
+        p.cache.k[at[0], 0, at[1], 0] = gap * np.log(2.0)
+        p.cache.v[at[0], 0, at[1]] = 0
+        q = torch.zeros(rows, heads, dim, dtype=t)
+        q[:, :, 0] = 1.0
+        out, lse = run_attention(attn, p, q, scale=1.0)
+        sample = sorted({0, rows // 2, rows - 1})
+        k, v = f64(p.cache.k), f64(p.cache.v)
+        n = keys + rows
+        lost = 0.0 if dt == "bf16" else 2.0 ** (-32 if rows * heads > 112 else -39)
+        for r in sample:
+            want, want_lse = oa.attention(f64(q[r:r + 1]), k, v, [0, 1], [keys + r + 1], p.table, 1.0)
+            e, ds = half_step(t), (n + 80) * U
+            assert want.min() > 2.0 ** -14   # no subnormal outputs
+            bound = e * want + (1 + e) * ((e + 2 * ds) * want + n * lost * v.max())
+            bad = np.abs(f64(out[r:r + 1]) - want) - bound
+            assert (bad <= 0).all(), (gap, r, (np.abs(f64(out[r:r + 1]) - want) / want).max())
+            assert np.abs(f64(lse[r:r + 1]) - want_lse).max() <= ds + 8 * U * np.abs(want_lse).max()
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_scores_of_many_millions(attn, rows, dt):
+    """Neighbouring scores in fp32 are up to 16 apart here: one key has it all, and no probability leaves the type."""
+    t, scale = TYPES[dt], 2.0 ** 10
+    for big in (2.0 ** 5, 2.0 ** 7 + 2.0 ** 3, 2.0 ** 8, 2.0 ** 8 + 2.0 ** 7):
+        case("millions", rows, dt, big)
+        p = Packed(attn, 61, [(rows, 700)], 1, 64, 16, t)
+        p.cache.k.zero_()
+        q = torch.zeros(rows, 1, 64, dtype=t)
+        q[:, :, 0] = 256.0
+        for key, share in ((5, 0.5), (300, 0.75), (611, 1.0)):   # step by step to scores of `big` 2^18
+            at = oa.place(0, key, p.table, 16, p.cache.k.shape[0])
+            p.cache.k[at[0], 0, at[1], 0] = share * big
+        out, lse = run_attention(attn, p, q, scale=scale)
+        at = oa.place(0, 611, p.table, 16, p.cache.k.shape[0])
+        # one probability of 1, in fp32: its product over its sum, rounded
+        want = p.cache.v[at[0], 0, at[1]].double().cpu().numpy()
+        assert (np.abs(f64(out) - want) <= (2 * half_step(t) + 4 * U) * np.abs(want)).all()
+        score = scale * 256.0 * big
+        assert (np.abs(f64(lse) - score) <= 16 * U * score).all()
