@@ -8,9 +8,9 @@
 // the row's maximum takes moves between few lanes, and what it holds after the exponential is its
 // operand of O^T = V^T P^T as it stands: which key a step's k-th place stands for is free as long as
 // both operands agree.  V^T is read from LDS through the transposing read.
-// That operand is rounded to the values' type, since the matrix units take both in one: each
-// probability by half a step of it, in fp16 by 2^-32 of the row's largest one at least; their sum is of the
-// unrounded ones, in fp32 like all else.
+// That operand is rounded to the values' type, since the matrix units take both in one.  Of few rows, what the rounding
+// leaves is multiplied too.  Of many rows, whose matrix steps bound them, it is lost: half a step of each probability,
+// relative, in fp16 up to 2^-32 of the row's largest one; their sum is of the unrounded ones, in fp32 like all else.
 //
 // Work is spread by the keys that there are, whatever the lengths: from all sequences' keys follows how many a
 // workgroup takes, so that those that run at once have as many each; a sequence's parts are joined by a second
@@ -36,7 +36,7 @@ constexpr int kPartKeys = 512;  // what beginning, writing and joining a part of
 // The exponent that probabilities are relative to, in log2: kAhead below a row's largest score when it was last raised, and
 // it is raised when that has grown by more than kSlack since.  bf16 has fp32's range.  In fp16 a probability is at most
 // 2^15, half of what the type holds, and what is lost below its smallest step is 2^-32 of the row's largest one, of few rows
-// (whose matrix steps wait for memory) 2^-39.  (Of many rows, 12 ahead and 3 of slack: 2000 tokens on 2000 of 16 / 4 heads of
+// (whose matrix steps wait for memory) 2^-38.  (Of many rows, 12 ahead and 3 of slack: 2000 tokens on 2000 of 16 / 4 heads of
 // 256 165 -> 182 us, 4000 on 4100 of 64 / 8 heads of 128 814 -> 820.)
 template <typename T, bool MANY>
 constexpr float kAhead = __is_same(T, f16) ? MANY ? 7.0f : 14.0f : 0.0f;
@@ -451,10 +451,32 @@ __device__ __forceinline__ f32x4 odd_values(const char* p, int d, int dim, bool 
 }
 
 // ------------------------------------------------------------------------ few rows
+// Two probabilities in two operands: cut off to the type, and what that leaves, which is at least `least`.  (Where an
+// infinite value meets it, it must be neither negative nor 0.)
+template <typename T>
+__device__ __forceinline__ void split(float a, float b, float least, uint32_t& w, uint32_t& rest) {
+  float ra, rb;
+  if constexpr (__is_same(T, f16)) {
+    w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+    // a mixed fma takes the halves as they are; the compiler converts them first
+    __asm__("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(ra) : "v"(w), "v"(a));
+    __asm__("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(rb) : "v"(w), "v"(b));
+  } else {
+    const uint32_t x = __builtin_bit_cast(uint32_t, a), y = __builtin_bit_cast(uint32_t, b);
+    w = __builtin_amdgcn_perm(y, x, 0x07060302);  // the upper halves
+    ra = a - __builtin_bit_cast(float, x & 0xFFFF0000u);
+    rb = b - __builtin_bit_cast(float, y & 0xFFFF0000u);
+  }
+  rest = Pair<T>::pack(fmaxf(ra, least), fmaxf(rb, least));
+}
+
 // 16 NT rows a workgroup; its W waves have the same rows and take turns at steps of 32 keys, each
 // with its own stages in LDS, filled by direct loads: the next step's keys are under way
 // from the products with this one's on, its values from their products on.  No wave waits for another until the
-// end, when the waves' sums are joined in LDS.  Bytes bound it: 32 sequences of one
+// end, when the waves' sums are joined in LDS.  The matrix steps wait for memory: a second product takes what the
+// rounding of the probabilities left, so that they count with twice the type's digits (blocks of 16 rows take as long as
+// without, of 32 2 to 3% more: 16 sequences of 9 rows over 2000 keys of 64 / 8 heads of 128 41 -> 42 us).  A step's values
+// are all in registers when the next ones are asked for, before their products.  Bytes bound it: 32 sequences of one
 // token over 1 to 8000 keys of 64 / 8 heads of 128, bf16, 113 us, 5.2 TB/s (a large copy reaches 5.1); one over 4000 keys of
 // 40 heads, fp16, 14 to 17 us, of which some 5 are the way to the first keys.
 template <typename T, int DP, int NT, int W>
@@ -602,7 +624,10 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
       reads_done();
       if (more) issue(k_head, k_lds, key + 32 * W, next);
       const bool masked = key + 32 > sight.full || here.there != ~0u;
-      u32x4 pr[NT];
+      // values of a step that not all rows see are cleared below; where they are not, all its keys are seen, or their values 0
+      const bool cleared = min(key + 32, sight.most) > sight.full;
+      const float least = cleared ? 0.0f : __is_same(T, f16) ? 0x1p-24f : 0x1p-126f;
+      u32x4 pr[NT], rest[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float x[8];
@@ -634,7 +659,12 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
           l[n] += x[i];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pr[n][i] = Pair<T>::pack(x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a, b;
+          split<T>(x[2 * i], x[2 * i + 1], least, a, b);
+          pr[n][i] = a;
+          rest[n][i] = b;
+        }
       }
       landed(more);  // the values; the next keys may be under way
       if (__builtin_expect(here.there != ~0u, 0)) {  // values that are none
@@ -642,17 +672,31 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
         for (int i = 0; i < kLoads; ++i)
           if (!(here.there >> (kPer * i + load_row) & 1)) *(u32x4*)(vs + 1024 * i + 16 * lane) = u32x4{0, 0, 0, 0};
       }
-      if (min(key + 32, sight.most) > sight.full) odd |= clear_odd<T, kLoads>(vs);
+      if (cleared) odd |= clear_odd<T, kLoads>(vs);
+      constexpr int kTogether = 8;  // operands of a step's products, all read before the last of them
+      static_assert(DP / 16 % kTogether == 0 || DP / 16 < kTogether, "whole sets");
 #pragma unroll
-      for (int d = 0; d < DP / 16; ++d) {
-        const uint8_t* const at = vs + (((int)(v_at - vs)) ^ (32 * d));
-        const u32x2 v0 = read_transposed(at), v1 = read_transposed(at + 16 * kRowBytes);
-        const u32x4 v = {v0[0], v0[1], v1[0], v1[1]};
+      for (int d0 = 0; d0 < DP / 16; d0 += kTogether) {
+        u32x4 v[kTogether < DP / 16 ? kTogether : DP / 16];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][d] = mfma16<T>(v, pr[n], o[n][d]);
+        for (int d = 0; d < kTogether && d0 + d < DP / 16; ++d) {
+          const uint8_t* const at = vs + (((int)(v_at - vs)) ^ (32 * (d0 + d)));
+          const u32x2 v0 = read_transposed(at), v1 = read_transposed(at + 16 * kRowBytes);
+          v[d] = u32x4{v0[0], v0[1], v1[0], v1[1]};
+        }
+        if (d0 + kTogether >= DP / 16) {
+          reads_done();
+          if (more) issue(v_head, v_lds, key + 32 * W, next);
+        }
+#pragma unroll
+        for (int d = 0; d < kTogether && d0 + d < DP / 16; ++d)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[n][d0 + d] = mfma16<T>(v[d], pr[n], o[n][d0 + d]);
+#pragma unroll
+        for (int d = 0; d < kTogether && d0 + d < DP / 16; ++d)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[n][d0 + d] = mfma16<T>(v[d], rest[n], o[n][d0 + d]);
       }
-      reads_done();
-      if (more) issue(v_head, v_lds, key + 32 * W, next);
       here = next;
     }
   }

@@ -170,10 +170,11 @@ lb_status littlebit_cache_append(const lb_cache *cache, const lb_cache_batch *ba
  *   lse        fp32 tokens x q->heads, or NULL: the logarithm of the sum of exp(scale q . k_j).
  *   ws         littlebit_cache_attention_workspace_bytes(...) bytes (may be 0, then ws may be
  *              NULL), 16-byte aligned.
- * Scores, softmax and sums are in fp32; the probabilities are rounded to the cache's type for
- * their product with the values (the matrix units take both in one type), each by half a step of
- * it.  In fp16, whose smallest step is a fixed one, those below 2^-21 of a row's largest are
- * rounded by 2^-32 of that one at most.  scale q . k_j is 10^8 at most in size.  The same call
+ * Scores, softmax and sums are in fp32.  The matrix units take probabilities and values in one
+ * type, the cache's: where sequences have more than some 80 rows x heads of a group on average, each
+ * probability is rounded to it for that product, by half a step (in fp16, whose smallest step is
+ * a fixed one, those below 2^-21 of a row's largest by up to 2^-32 of that one); with fewer, what
+ * the rounding leaves is multiplied too.  scale q . k_j is 10^8 at most in size.  The same call
  * gives the same bits.
  * tokens x q->heads <= 2^30, fewer where the grid holds no more.
  */

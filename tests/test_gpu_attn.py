@@ -941,3 +941,42 @@ def test_scores_of_many_millions(attn, rows, dt):
         assert (np.abs(f64(out) - want) <= (2 * half_step(t) + 4 * U) * np.abs(want)).all()
         score = scale * 256.0 * big
         assert (np.abs(f64(lse) - score) <= 16 * U * score).all()
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("seqs,rows,heads,dim", [(40, 1, 4, 64), (12, 16, 1, 128), (6, 30, 1, 128), (10, 9, 2, 256), (8, 100, 1, 64), (6, 24, 2, 80)])
+def test_few_rows_are_rounded_once(attn, seqs, rows, heads, dim, dt):
+    """Of few rows nothing but the output is rounded to the type: beside that rounding what is computed in fp32 is small.  An
+    output whose exact value lies within an error d of the middle between two neighbours a step s apart may fall to the other
+    one: a share 2 d / s of them, a step off each, while roundings are s / sqrt(12) in the mean.  Here d is some 10 u of the
+    values' mean size, which is up to 9 times the outputs' for 64 to 164 keys: 2 d / s below 180 u / 2^-11 = 0.022 for fp16,
+    less for bf16.  (Probabilities of half a step e would be off by e / sqrt(3) each: d = e / 2, and a share of 1 / 4 and more.)"""
+    t = TYPES[dt]
+    case("rounded once", seqs, rows, heads, dim, dt)
+    p = Paged(attn, 70, [(rows, 64)] * seqs, 1, dim, 16, t)
+    q = randn(71, p.tokens, heads, dim, scale=0.3).to(t)
+    out, _ = run_attention(attn, p, q)
+    want, _ = oa.attention(f64(q), f64(p.cache.k), f64(p.cache.v), p.starts, p.lens, p.table, dim ** -0.5)
+    nearest = f64(torch.from_numpy(want).to(t))
+    rounding = np.sqrt(np.mean((nearest - want) ** 2))
+    others = np.sqrt(np.mean((f64(out) - nearest) ** 2))
+    print("others / rounding", others / rounding)
+    assert others <= np.sqrt(0.022 * 12) * rounding
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("rows,cached,heads,dim", [(1, 90, 1, 64), (1, 3000, 4, 128), (30, 700, 1, 128), (9, 400, 2, 256), (200, 1500, 1, 128)])
+def test_an_infinite_value_that_all_rows_see_is_alone_in_its_channel(attn, rows, cached, heads, dim, dt):
+    """That channel's outputs are that infinity, NaN for both signs; all others keep their bits."""
+    case("alone", rows, cached, heads, dim, dt)
+    p = Paged(attn, 72, [(rows, cached), (1, 40)], 1, dim, 16, TYPES[dt])
+    q = randn(73, p.tokens, heads, dim, scale=0.3).to(p.t)
+    clean, clean_lse = run_attention(attn, p, q)
+    inf = float("inf")
+    for key, channel, value in ((3, 9, inf), (cached // 2, 9, inf), (cached // 2, 30, -inf), (cached - 1, 41, inf), (0, 41, -inf), (64, 55, float("nan"))):
+        a = oa.place(0, key, p.table, 16, p.cache.k.shape[0])
+        p.cache.v[a[0], :, a[1], channel] = value
+    out, lse = run_attention(attn, p, q)
+    assert (out[:rows, :, 9] == inf).all() and (out[:rows, :, 30] == -inf).all() and torch.isnan(out[:rows, :, [41, 55]]).all()
+    rest = [d for d in range(dim) if d not in (9, 30, 41, 55)]
+    assert torch.equal(out[:rows, :, rest], clean[:rows, :, rest]) and torch.equal(out[rows:], clean[rows:]) and torch.equal(lse, clean_lse)
