@@ -435,6 +435,14 @@ __device__ __forceinline__ bool clear_odd(uint8_t* stage) {
   }
   return true;
 }
+// 0 where a key at `p` has an infinity or a NaN, else 1.  A finite score has a probability, however small, and an infinite
+// value with it is infinite; with such a key the score is none, or infinite: 0 or more times infinity, or a row without a sum.
+template <typename T>
+__device__ __forceinline__ float is_even(const char* p, int dim) {
+  const int d = 4 * (threadIdx.x & 63);
+  const u32x2 k = d < dim ? *(const u32x2*)(p + 2 * d) : u32x2{0, 0};
+  return __ballot(odd_word<T>(k[0]) || odd_word<T>(k[1])) ? 0.0f : 1.0f;
+}
 // The four values of channels d to d + 3 of a row at `p` that are odd, 0 in the place of the others.
 template <typename T>
 __device__ __forceinline__ f32x4 odd_values(const char* p, int d, int dim, bool there) {
@@ -710,12 +718,13 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
 #pragma unroll 1
       for (int r = 0; r < 32; ++r) {
         const int eight = r >> 3, id = eight == 0 ? t.id[0] : eight == 1 ? t.id[1] : eight == 2 ? t.id[2] : t.id[3];
-        const char* const src = v_head + id * P.page + ((at + r) & mask) * P.slot;
+        const long src = id * P.page + ((at + r) & mask) * P.slot;
+        const float one = is_even<T>(k_head + src, A.dim);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const bool mine = seen(n, at, t.there) >> r & 1;
 #pragma unroll
-          for (int d = 0; d < DP / 16; ++d) o[n][d] += odd_values<T>(src, 16 * d + 4 * g, A.dim, mine);
+          for (int d = 0; d < DP / 16; ++d) o[n][d] += one * odd_values<T>(v_head + src, 16 * d + 4 * g, A.dim, mine);
         }
       }
     }
@@ -1087,13 +1096,14 @@ __global__ __launch_bounds__(64 * W, DP == 256 ? 1 : 2) void lb_attn_tile_kernel
 #pragma unroll 1
         for (int r = 0; r < 32; ++r) {
           const int page = page_at(at + r);
-          const char* const src = v_head + (is_page(page) ? page : 0) * P.page + ((at + r) & mask) * P.slot;
+          const long src = (is_page(page) ? page : 0) * P.page + ((at + r) & mask) * P.slot;
+          const float one = is_even<T>(k_head + src, A.dim);
           const bool mine = seen(at, there) >> r & 1;
 #pragma unroll
           for (int d = 0; d < kD; ++d)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const f32x4 f = odd_values<T>(src, 32 * d + 8 * i + 4 * h, A.dim, mine);
+              const f32x4 f = one * odd_values<T>(v_head + src, 32 * d + 8 * i + 4 * h, A.dim, mine);
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[d][4 * i + e] += f[e];
             }

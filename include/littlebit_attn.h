@@ -163,7 +163,9 @@ lb_status littlebit_cache_append(const lb_cache *cache, const lb_cache_batch *ba
  *   tree       int64 [tokens]: those whose bit j - (len - n) is set in the row's word, so
  *              that each row of a tree of drafts names its ancestors and itself.  A
  *              sequence has at most LB_TREE_MAX rows then; keys of later ones are not seen.
- * What a row does not see has no part in its output, NaN and infinities in it included.
+ * What a row does not see has no part in its output, NaN and infinities in it included.  An
+ * infinite value that it sees is infinite there, NaN where its score is -infinity, or so low that
+ * the type or fp32 may hold no more of its probability.
  * A row that sees nothing has output 0 and lse -infinity.
  *   scale      finite, 1e30 at most in size; may be negative or 0.
  *   out        as q; overlaps no input.

@@ -980,3 +980,26 @@ def test_an_infinite_value_that_all_rows_see_is_alone_in_its_channel(attn, rows,
     assert (out[:rows, :, 9] == inf).all() and (out[:rows, :, 30] == -inf).all() and torch.isnan(out[:rows, :, [41, 55]]).all()
     rest = [d for d in range(dim) if d not in (9, 30, 41, 55)]
     assert torch.equal(out[:rows, :, rest], clean[:rows, :, rest]) and torch.equal(out[rows:], clean[rows:]) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+@pytest.mark.parametrize("rows,cached,heads,dim", [(7, 40, 2, 64), (7, 40, 1, 72), (30, 200, 1, 128), (9, 1200, 2, 256), (200, 100, 1, 64), (300, 40, 1, 128), (300, 4200, 2, 128), (150, 1030, 1, 256)])
+def test_an_infinite_value_of_no_probability_is_not_a_number(attn, rows, cached, heads, dim, dt):
+    """0 times infinity, as in the formula, in steps that all rows see and in those that some do: of keys whose score is
+    -infinity.  Others give that infinity."""
+    case("no probability", rows, cached, heads, dim, dt)
+    t = TYPES[dt]
+    p = Paged(attn, 80, [(rows, cached), (2, 9)], 1, dim, 8, t)
+    q = randn(81, p.tokens, heads, dim, scale=0.5).abs().to(t)   # all scores of the keys below are of one sign
+    inf = float("inf")
+    for key, channel, k in ((3, 9, -inf), (cached + 1, 20, -inf), (cached + rows // 2, 33, -inf), (cached + rows - 2, 5, -inf), (cached + rows // 2 + 1, 50, 0.0)):
+        a = oa.place(0, key, p.table, 8, p.cache.k.shape[0])
+        p.cache.k[a[0], :, a[1]] = k
+        p.cache.v[a[0], :, a[1], channel] = inf
+    out, _ = run_attention(attn, p, q)
+    with np.errstate(invalid="ignore"):
+        want, _ = oa.attention(f64(q), f64(p.cache.k), f64(p.cache.v), p.starts, p.lens, p.table, dim ** -0.5)
+    got = f64(out)
+    assert np.isnan(want[rows - 1, :, [5, 9, 20, 33]]).all() and np.isposinf(want[rows - 1, :, 50]).all() and np.isfinite(want[0, :, [5, 20, 33]]).all()
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isposinf(got), np.isposinf(want))
+    assert not np.isneginf(got).any()
