@@ -310,6 +310,16 @@ def littlebit_rope_bwd(dq: Optional[torch.Tensor], dk: Optional[torch.Tensor], p
 
 # ---------------------------------------------------------------------------------------------------- the cache
 
+def _used(shape, strides):
+    """Strides with those of dimensions of size one, which no address uses, as in a contiguous tensor."""
+    out, inner = list(strides), 1
+    for i in range(len(shape) - 1, -1, -1):
+        if shape[i] == 1:
+            out[i] = inner
+        inner = max(inner, out[i] * shape[i])
+    return tuple(out)
+
+
 @dataclass
 class LittleBitCache:
     """Pages of keys and of values, pages x heads x slots x dim each (fp16 or
@@ -328,9 +338,13 @@ class LittleBitCache:
         code = _HALF.get(k.dtype) if torch.is_tensor(k) else None
         if code is None or not torch.is_tensor(v) or k.dim() != 4 or k.get_device() < 0:
             raise ValueError("a cache is two pages x heads x slots x dim CUDA tensors of float16 or bfloat16")
-        strides = k.stride()
-        if v.dtype is not k.dtype or v.get_device() != k.get_device() or v.shape != k.shape or v.stride() != strides:
-            raise ValueError("the cache's values must have the keys' type, device, shape and strides")
+        if v.dtype is not k.dtype or v.get_device() != k.get_device() or v.shape != k.shape:
+            raise ValueError("the cache's values must have the keys' type, device and shape")
+        strides, others = k.stride(), v.stride()
+        if strides != others or 1 in k.shape:
+            strides, others = _used(k.shape, strides), _used(k.shape, others)
+            if strides != others:
+                raise ValueError("the cache's values must have the keys' strides")
         if strides[3] != 1:
             raise ValueError("the cache's channels must lie together")
         return _Cache(k.data_ptr(), v.data_ptr(), *strides[:3], *k.shape, code)

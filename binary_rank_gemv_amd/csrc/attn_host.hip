@@ -79,6 +79,11 @@ lb_status check_heads(const char* name, const char* what, const lb_heads* h, int
   return LB_OK;
 }
 
+// Whether two tensors of heads have the same strides, where more than one token or head uses them.
+bool same_strides(const lb_heads* a, const lb_heads* b, int64_t tokens) {
+  return (tokens == 1 || a->token_stride == b->token_stride) && (a->heads == 1 || a->head_stride == b->head_stride);
+}
+
 // An output beside its input: as many heads, and in place only with the same strides.
 lb_status check_pair(const char* name, const char* what, const lb_heads* in, const char* out_what, const lb_heads* out,
                      int64_t tokens, int dim) {
@@ -86,7 +91,7 @@ lb_status check_pair(const char* name, const char* what, const lb_heads* in, con
   LB_TRY(check_heads(name, out_what, out, tokens, dim, true));
   if (in->heads != out->heads)
     return fail(LB_ERR_INVALID_ARG, "%s: %s has %d heads, %s %d", name, what, in->heads, out_what, out->heads);
-  if (tokens > 0 && in->p == out->p && (in->token_stride != out->token_stride || in->head_stride != out->head_stride))
+  if (tokens > 0 && in->p == out->p && !same_strides(in, out, tokens))
     return fail(LB_ERR_INVALID_ARG, "%s: %s in place needs the same strides", name, out_what);
   return LB_OK;
 }
@@ -255,8 +260,7 @@ lb_status littlebit_rope_bwd(const lb_heads* dq, const lb_heads* dk, const lb_he
       LB_TRY(check_heads(name, names[i][1], x[i], tokens, dim, false));
       if (x[i]->heads != dy[i]->heads)
         return fail(LB_ERR_INVALID_ARG, "%s: %s has %d heads, %s %d", name, names[i][1], x[i]->heads, names[i][0], dy[i]->heads);
-      if (tokens > 0 && x[i]->p == dx[i]->p &&
-          (x[i]->token_stride != dx[i]->token_stride || x[i]->head_stride != dx[i]->head_stride))
+      if (tokens > 0 && x[i]->p == dx[i]->p && !same_strides(x[i], dx[i], tokens))
         return fail(LB_ERR_INVALID_ARG, "%s: %s in place needs the same strides", name, names[i][2]);
       a.x[i] = x[i]->p; a.xt[i] = x[i]->token_stride; a.xh[i] = x[i]->head_stride;
       a.weight[i] = weight[i];

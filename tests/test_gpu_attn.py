@@ -1003,3 +1003,29 @@ def test_an_infinite_value_of_no_probability_is_not_a_number(attn, rows, cached,
     assert np.isnan(want[rows - 1, :, [5, 9, 20, 33]]).all() and np.isposinf(want[rows - 1, :, 50]).all() and np.isfinite(want[0, :, [5, 20, 33]]).all()
     assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isposinf(got), np.isposinf(want))
     assert not np.isneginf(got).any()
+
+
+def test_strides_that_no_address_uses(attn):
+    """Those of a single page, head or token: keys and values may differ in them, and an output from its input in place."""
+    for pages, heads, page in ((6, 1, 16), (1, 3, 64), (1, 1, 64)):
+        case("unused strides", pages, heads)
+        k, v = (randn(i, pages, heads, page, 64).half().cuda() for i in (1, 2))
+        table = ints([list(range(pages))])
+        batch = attn.CacheBatch(ints([0, 1]), ints([pages * page - 3]), table)
+        q = randn(3, 1, 2 * heads, 64).half().cuda()
+        want = attn.littlebit_cache_attention_fwd(q, attn.LittleBitCache(k, v), batch)
+        odd = [5 if n == 1 else s for n, s in zip(k.shape, k.stride())]
+        for a, b in ((k.as_strided(k.shape, odd), v), (k, v.as_strided(v.shape, odd)), (k.as_strided(k.shape, odd), v.as_strided(v.shape, odd))):
+            assert torch.equal(attn.littlebit_cache_attention_fwd(q, attn.LittleBitCache(a, b), batch), want)
+    w = torch.ones(64, dtype=torch.float16, device="cuda")
+    for shape, strides in (((1, 3, 64), (1000, 64, 1)), ((4, 1, 64), (64, 7, 1)), ((1, 1, 64), (3, 9, 1))):
+        x = randn(4, *shape).half().cuda()
+        want, _ = attn.littlebit_rope_fwd(x, None, q_weight=w)
+        dx, _, dw, _ = attn.littlebit_rope_bwd(x, None, q=x, q_weight=w)
+        y = x.clone()
+        got, _, dw2, _ = attn.littlebit_rope_bwd(x, None, q=y, q_weight=w, dq_in=y.as_strided(shape, strides))
+        assert torch.equal(y, dx) and torch.equal(dw2, dw)
+        attn.littlebit_rope_fwd(x, None, q_weight=w, q_out=x.as_strided(shape, strides))
+        assert torch.equal(x, want)
+    with pytest.raises(ValueError, match="strides"):
+        attn.LittleBitCache(torch.empty(2, 1, 64, 64, dtype=torch.float16, device="cuda"), torch.empty(2, 1, 64, 72, dtype=torch.float16, device="cuda")[..., :64]).c_struct()
