@@ -483,9 +483,10 @@ class LittleBitAttention:
         """x (tokens x n, fp16) of the batch's rows -> tokens x o.m.  Appends the
         rows' keys and values to the cache.  positions (int32) is what inv_freq needs."""
         rows = lambda layer: littlebit_linear_fwd(layer, x).view(x.shape[0], layer.m // self.dim, self.dim)  # noqa: E731
-        q, k, v = rows(self.q), rows(self.k), rows(self.v)
-        q = littlebit_cache_append(cache, batch, k, v, q, positions, self.inv_freq, self.q_norm, self.k_norm, self.eps,
-                                   self.interleaved, q_out=q)
-        out = torch.zeros_like(q)   # rows of no sequence stay 0
-        littlebit_cache_attention_fwd(q, cache, batch, tree, self.scale, out=out)
-        return littlebit_linear_fwd(self.o, out.view(x.shape[0], -1))
+        with torch.cuda.device_of(x):   # the layers run on the current device
+            q, k, v = rows(self.q), rows(self.k), rows(self.v)
+            q = littlebit_cache_append(cache, batch, k, v, q, positions, self.inv_freq, self.q_norm, self.k_norm, self.eps,
+                                       self.interleaved, q_out=q)
+            out = torch.zeros_like(q)   # rows of no sequence stay 0
+            littlebit_cache_attention_fwd(q, cache, batch, tree, self.scale, out=out)
+            return littlebit_linear_fwd(self.o, out.view(x.shape[0], -1))

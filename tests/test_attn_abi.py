@@ -189,3 +189,30 @@ def test_binding_refuses_what_is_not_on_a_gpu():
                  lambda: attn.littlebit_cache_accept(cache, batch, i[None])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_block_calls_its_layers_on_the_device_of_its_tensors(monkeypatch):
+    """The layers run on the current device: the block makes that of x current, also where it is another."""
+    inside, calls = [], []
+
+    class Device:
+        def __enter__(self):
+            inside.append(True)
+
+        def __exit__(self, *_):
+            inside.pop()
+
+    def layer(name, m):
+        return type("Layer", (), {"name": name, "m": m})()
+
+    def linear(layer, x):
+        calls.append((layer.name, bool(inside)))
+        return x.new_zeros(x.shape[0], layer.m)
+
+    monkeypatch.setattr(torch.cuda, "device_of", lambda x: Device())
+    monkeypatch.setattr(attn, "littlebit_linear_fwd", linear)
+    monkeypatch.setattr(attn, "littlebit_cache_append", lambda cache, batch, k, v, q, *rest, q_out: q_out)
+    monkeypatch.setattr(attn, "littlebit_cache_attention_fwd", lambda q, *rest, out: out)
+    block = attn.LittleBitAttention(layer("q", 16), layer("k", 8), layer("v", 8), layer("o", 12), 8, None)
+    assert block(torch.zeros(3, 12), None, None).shape == (3, 12)
+    assert sorted(calls) == [("k", True), ("o", True), ("q", True), ("v", True)] and not inside
