@@ -1143,18 +1143,16 @@ __global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, i
   const int step = A.kv_heads * rows, count_of = r.count & 0xFFFF, seq = r.count >> 16 & 0xFFFF;
   bool several = lane < per && mine < all_rows && count_of > 1 && seq < A.pages.seqs;
   several = several && r.first >= 0 && r.first + (count_of - 1l) * step < limit;
-  if (several) {
-    // a row of no sequence has no record, and what lies in its place may be an earlier call's: a record stands if its
-    // sequence has the row in this call, which has written it then
-    const Span s = span_of(A.pages, seq, (int)A.tokens);
-    const int token = (int)(mine / A.heads);
-    several = token >= s.start && token < s.start + s.rows;
-  }
+  typedef const __attribute__((address_space(4))) int32_t* Ints;  // read by the scalar unit
+  const Ints starts = (Ints)(uintptr_t)A.pages.starts, lens = (Ints)(uintptr_t)A.pages.lens;
   const int set = lane / LD, d = 4 * (lane % LD);
   const bool in = d < A.dim;
   for (uint64_t left = __ballot(several); left; left &= left - 1) {
     const int l = __builtin_ctzll(left);
     const int first = __builtin_amdgcn_readlane(r.first, l), count = __builtin_amdgcn_readlane(count_of, l);
+    // A row of no sequence has no record, and what lies in its place may be an earlier call's: a record stands if its
+    // sequence has the row in this call, which has written it then.  Asked for here, looked at behind the sums.
+    const int of = __builtin_amdgcn_readlane(seq, l), start = starts[of], end = starts[of + 1], len = lens[of];
     float top = -INFINITY, total = 0.0f;
     f32x4 sum = {0, 0, 0, 0};
     // eight sets' loads at a time; behind the last part it again, with factor 0
@@ -1199,9 +1197,10 @@ __global__ __launch_bounds__(256) void lb_attn_join_kernel(const LbAttnArgs A, i
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] += lane_xor<32>(sum[e]);
     }
-    if (set == 0) {
-      const long row = row0 + l;
-      const int t = (int)(row / A.heads);
+    const long row = row0 + l;
+    const int t = (int)(row / A.heads);
+    const Span s = span_of(A.pages, start, end, len, (int)A.tokens);
+    if (set == 0 && t >= s.start && t < s.start + s.rows) {
       store_result<T>(A, t, (int)(row - (long)t * A.heads), d, sum, top, total);
     }
   }

@@ -32,16 +32,18 @@ struct Span {
   int keys;    // keys of it that its columns can hold
   int base;    // keys before its rows (less than 0 where lens is wrong: those do not exist)
 };
-__device__ __forceinline__ Span span_of(const LbPages& P, int seq, int tokens) {
+__device__ __forceinline__ Span span_of(const LbPages& P, int start, int end, int len, int tokens) {
   Span s;
-  s.start = P.starts[seq];
-  const int end = P.starts[seq + 1], len = P.lens[seq];
-  const bool fine = s.start >= 0 && s.start < tokens && end > s.start && len >= 0;
-  const int rows = fine ? end - s.start : 0;
+  s.start = start;
+  const bool fine = start >= 0 && start < tokens && end > start && len >= 0;
+  const int rows = fine ? end - start : 0;
   s.base = fine ? len - rows : 0;
-  s.rows = fine ? min(rows, tokens - s.start) : 0;
+  s.rows = fine ? min(rows, tokens - start) : 0;
   s.keys = fine ? min(len, P.columns << P.shift) : 0;
   return s;
+}
+__device__ __forceinline__ Span span_of(const LbPages& P, int seq, int tokens) {
+  return span_of(P, P.starts[seq], P.starts[seq + 1], P.lens[seq], tokens);
 }
 
 // Where the page of a key begins, in pages; less than 0 where it has none.
