@@ -486,7 +486,7 @@ __device__ __forceinline__ void split(float a, float b, float least, uint32_t& w
 // without, of 32 2 to 3% more: 16 sequences of 9 rows over 2000 keys of 64 / 8 heads of 128 41 -> 42 us).  A step's values
 // are all in registers when the next ones are asked for, before their products.  Bytes bound it: 32 sequences of one
 // token over 1 to 8000 keys of 64 / 8 heads of 128, bf16, 113 us, 5.2 TB/s (a large copy reaches 5.1); one over 4000 keys of
-// 40 heads, fp16, 14 to 17 us, of which some 5 are the way to the first keys.
+// 40 heads, fp16, 18 us, of which some 5 are the way to the first keys.
 template <typename T, int DP, int NT, int W>
 __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream_kernel(const LbAttnArgs A) {
   constexpr int kRowBytes = 2 * DP, kPieces = DP / 8, kStage = 32 * kRowBytes;
@@ -774,10 +774,10 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
 // Keys have two stages, values three: a tile's values are read until one step after its keys.  One barrier a tile,
 // where the next tile has landed; the one after it is then asked for.
 //
-// bf16, 64 / 8 heads of 128: a prompt of 4000 tokens over 4100 cached ones 810 us, 0.99 PFLOP/s (1.04 for 16384 tokens of
-// 32 / 8), where a large library product runs at 1.23 and a loop of this kernel's instructions alone, without barriers, at
-// 1.32.  Slower were halves of the waves a step apart (916 us), tiles asked for two ahead (833), and the compiler's own
-// order of a step (850 to 870).
+// bf16, 64 / 8 heads of 128: a prompt of 4000 tokens over 4100 cached ones 765 to 805 us by the card's clock, 0.99 to 1.05
+// PFLOP/s (1.06 for 16384 tokens of 32 / 8), where a large library product runs at 1.23 and a loop of this kernel's
+// instructions alone, without barriers, at 1.32.  Slower, each beside this form's 804 to 823 us of the same day, were halves of
+// the waves a step apart (916), tiles asked for two ahead (833), and the compiler's own order of a step (850 to 870).
 template <typename T>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   if constexpr (__is_same(T, f16))

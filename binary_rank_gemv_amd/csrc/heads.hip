@@ -209,9 +209,9 @@ __device__ __forceinline__ float head_scale(const float (&a)[8], const float (&b
 // ------------------------------------------------------------------------ forward
 
 // A wave: one token, `span` steps of 64 / LG heads; the queries' steps first, then the
-// keys', then the values'.  APPEND: keys and values go to their page.  Bytes bound it: 4000 tokens of 64 and 8 heads of
-// 128, bf16, normed, 33 us, 4.5 TB/s (a large copy reaches 5.1); 2039 into a cache, interleaved, 17.5 us, 4.8 TB/s; one
-// token of 40 heads 4.2 us, latency.
+// keys', then the values'.  APPEND: keys and values go to their page.  Bytes bound it.  With inputs from memory (six sets
+// in turn, more than the caches hold): 4000 tokens of 64 and 8 heads of 128, bf16, normed, 33 us, 4.5 TB/s (a large copy
+// reaches 5.1); 2039 into a cache, interleaved, 20 us, 4.1 TB/s; one token of 40 heads 3.8 us, latency.
 template <typename T, int LG, bool INTER, bool VEC, bool APPEND>
 __global__ __launch_bounds__(256) void lb_rope_kernel(const LbRopeArgs A) {
   __shared__ float2 cs_all[4][kMaxPairs];
@@ -291,8 +291,9 @@ void launch_one(LbRopeArgs& a, hipStream_t stream) {
   int steps = 0;
   for (int i = 0; i < 3; ++i) steps += (a.heads[i] + kHeads - 1) / kHeads;
   // one step a wave while there are few tokens, so that a call is short; with more, a wave takes some of
-  // its token's heads and computes the turns, and to a cache the slot, once for them.  4000 tokens of 64 and 8 heads, bf16,
-  // normed: 2, 3, 5 and 9 steps 27.6, 26.4, 26.9 and 28.5 us; 2039 to a cache 19.9, 19.3, 17.8 and 17.8.
+  // its token's heads and computes the turns, and to a cache the slot, once for them.  With inputs from
+  // memory, bf16, normed, 2, 3, 5 and 9 steps: 4000 tokens of 64 and 8 heads 34.0, 33.5, 34.8 and 34.8 us, 2039 to a cache
+  // 22.1, 23.2, 20.9 and 21.0.  (500 of 40 and 40 heads 8.4, 8.9, 10.9 and 10.8.)
   const long most = APPEND ? 5 : 3;
   a.blocks = a.tokens * steps <= 2048 ? steps : (steps + most - 1) / most;
   while (a.tokens * a.blocks > 1 << 25) a.blocks = (a.blocks + 1) / 2;  // a grid holds fewer than 2^32 threads
@@ -454,7 +455,7 @@ __global__ __launch_bounds__(256) void lb_rope_bwd_kernel(const LbRopeBwdArgs A)
 }
 
 // dweight = sum of the workgroups' partial sums: 16 columns x 64 slices of workgroups,
-// joined in order.  Latency bounds it, 4 us.
+// joined in order.  Latency bounds it, 3 to 5 us.
 __global__ __launch_bounds__(1024) void lb_rope_dweight_kernel(const LbRopeBwdArgs A) {
   __shared__ float s[64][17];
   const int part = blockIdx.y;
@@ -561,8 +562,8 @@ hipError_t lb_launch_rope(LbRopeArgs& a, int dtype, hipStream_t stream) {
 }
 
 // Workgroups of the backward pass, a function of the sizes alone (the sums and the workspace are the same on
-// every part): one step a wave up to four workgroups a compute unit (4000 tokens of 64 and 8 heads, bf16, with the second
-// kernel: 512, 1024 and 2048 workgroups 63, 54 and 55 us).
+// every part): one step a wave up to four workgroups a compute unit (with the second kernel, inputs from memory: 512, 1024
+// and 2048 workgroups 64, 58 and 57 us for 4000 tokens of 64 and 8 heads, bf16, 33, 30 and 33 for 8000 of 8 and 8).
 void lb_rope_bwd_groups(int64_t tokens, int heads, int kv_heads, int dim, int* groups) {
   const int per = 64 / (dim <= 64 ? 4 : dim <= 128 ? 8 : 16);
   const int64_t a = tokens * ((heads + per - 1) / per), b = tokens * ((kv_heads + per - 1) / per);

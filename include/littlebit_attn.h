@@ -148,7 +148,7 @@ lb_status littlebit_rope_bwd(const lb_heads *dq, const lb_heads *dk, const lb_he
  *   q, q_out   as for littlebit_rope_fwd, or both NULL.
  *   rope       NULL: keys and queries are stored as they are.
  * Two rows of a call that fall on one slot (sequences that share the page they end in)
- * leave either's values there.
+ * leave values of either there, piece by piece.
  */
 lb_status littlebit_cache_append(const lb_cache *cache, const lb_cache_batch *batch, int64_t tokens,
                                  const lb_heads *k, const lb_heads *v, const lb_heads *q,
