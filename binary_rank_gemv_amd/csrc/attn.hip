@@ -482,11 +482,11 @@ __device__ __forceinline__ void split(float a, float b, float least, uint32_t& w
 // with its own stages in LDS, filled by direct loads: the next step's keys are under way
 // from the products with this one's on, its values from their products on.  No wave waits for another until the
 // end, when the waves' sums are joined in LDS.  The matrix steps wait for memory: a second product takes what the
-// rounding of the probabilities left, so that they count with twice the type's digits (blocks of 16 rows take as long as
-// without, of 32 2 to 3% more: 16 sequences of 9 rows over 2000 keys of 64 / 8 heads of 128 41 -> 42 us).  A step's values
-// are all in registers when the next ones are asked for, before their products.  Bytes bound it: 32 sequences of one
-// token over 1 to 8000 keys of 64 / 8 heads of 128, bf16, 113 us, 5.2 TB/s (a large copy reaches 5.1); one over 4000 keys of
-// 40 heads, fp16, 18 us, of which some 5 are the way to the first keys.
+// rounding of the probabilities left, so that they count with twice the type's digits (0.2 us of a call of 20 in blocks of
+// 16 rows, 3% in blocks of 32: 16 sequences of 9 rows over 2000 keys of 64 / 8 heads of 128 40 -> 41).  A step's keys, and
+// its values, are all in registers before their products; the next values are asked for then.  Bytes bound it: 32
+// sequences of one token over 1 to 8000 keys of 64 / 8 heads of 128, bf16, 113 us, 5.2 TB/s (a large copy reaches 5.1); one
+// over 4000 keys of 40 heads, fp16, 18 us, of which some 5 are the way to the first keys.
 template <typename T, int DP, int NT, int W>
 __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream_kernel(const LbAttnArgs A) {
   constexpr int kRowBytes = 2 * DP, kPieces = DP / 8, kStage = 32 * kRowBytes;
@@ -620,14 +620,21 @@ __global__ __launch_bounds__(64 * W, DP * NT <= 256 ? 2 : 1) void lb_attn_stream
 #pragma unroll
       for (int n = 0; n < NT; ++n) st[n][0] = st[n][1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int s = 0; s < DP / 32; ++s) {
-        const uint8_t* const at = ks + (((int)(k_at - ks)) ^ (64 * s));
-        const u32x4 k0 = *(const u32x4*)at, k1 = *(const u32x4*)(at + 16 * kRowBytes);
+      for (int s0 = 0; s0 < DP / 32; s0 += 4) {
+        u32x4 kf[4][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          st[n][0] = mfma16<T>(k0, q[n][s], st[n][0]);
-          st[n][1] = mfma16<T>(k1, q[n][s], st[n][1]);
+        for (int s = 0; s < 4 && s0 + s < DP / 32; ++s) {
+          const uint8_t* const at = ks + (((int)(k_at - ks)) ^ (64 * (s0 + s)));
+          kf[s][0] = *(const u32x4*)at;
+          kf[s][1] = *(const u32x4*)(at + 16 * kRowBytes);
         }
+#pragma unroll
+        for (int s = 0; s < 4 && s0 + s < DP / 32; ++s)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            st[n][0] = mfma16<T>(kf[s][0], q[n][s0 + s], st[n][0]);
+            st[n][1] = mfma16<T>(kf[s][1], q[n][s0 + s], st[n][1]);
+          }
       }
       reads_done();
       if (more) issue(k_head, k_lds, key + 32 * W, next);
